@@ -305,6 +305,145 @@ typedef enum sherry_prefill_kernel {
 } sherry_prefill_kernel;
 sherry_status sherry_set_prefill_kernel(sherry_prefill_kernel kind);
 
+/* ---- Attention on a 4-bit key/value cache: what a decoder layer runs between
+ * its q|k|v product and its o product.  (The Sherry paper covers the weights;
+ * these operators are this library's own, for decoding with them.)
+ *
+ * Shared conventions.  A buffer of heads is [token][head][head_dim] with any
+ * token and head stride in elements (so slices of a fused q|k|v output are
+ * taken as they lie) and unit stride along head_dim; its address and strides
+ * are multiples of 16 bytes.  Index buffers (positions, slots, tables,
+ * lengths) are read on the device: entries out of range are never followed
+ * (each entry point says what they give instead).  A call with nothing to do
+ * (n = 0) returns SHERRY_OK and enqueues nothing, whatever its pointers. */
+
+/* One side of sherry_qk_norm_rope (HOST struct of DEVICE pointers). */
+typedef struct {
+  const void* x;    /* in: n tokens x heads */
+  void* y;          /* out; may be x itself with the same strides and dtype */
+  const float* w;   /* head_dim norm weights, 16-byte aligned, or NULL: no norm */
+  int64_t x_stride_token, x_stride_head; /* elements */
+  int64_t y_stride_token, y_stride_head;
+  int32_t heads;
+} sherry_heads;
+
+/* RMS norm of every query and key head and the rotation of its position, in
+ * one pass:
+ *   v    = x * (1 / sqrt(mean(x^2) + eps)) * w              (v = x without w)
+ *   y    = (a cos - b sin, b cos + a sin) for each pair (a, b) of the first
+ *          rot_dim values of v; the others as they are
+ * in fp32, rounded once to y_dt.
+ *   q, k       : the two sides; k may be NULL
+ *   x_dt, y_dt : F32|F16|BF16 each
+ *   head_dim   : a multiple of 16, at most 256
+ *   rot_dim    : a multiple of 16, 16..head_dim
+ *   interleaved: 0 pairs (i, i + rot_dim/2), 1 pairs (2i, 2i + 1)
+ *   cos, sin   : max_pos x rot_dim/2 fp32, 16-byte aligned; row p holds the
+ *                angles of position p
+ *   positions  : n int64; one outside [0, max_pos) gives NaN in the rotated
+ *                values of its token
+ * Errors: EINVAL null pointer, n < 0, heads, max_pos, head_dim or rot_dim <= 0;
+ * EDTYPE; ESHAPE other head_dim or rot_dim, negative stride, size overflow;
+ * EALIGN. */
+sherry_status sherry_qk_norm_rope(const sherry_heads* q /* HOST */, const sherry_heads* k /* HOST */, sherry_dtype x_dt,
+                                  sherry_dtype y_dt, int64_t n, int32_t head_dim, int32_t rot_dim, int32_t interleaved,
+                                  const float* cos, const float* sin, int64_t max_pos, const int64_t* positions,
+                                  float eps, hipStream_t stream);
+
+/* A paged cache of keys and values in 4 bits (HOST struct).  For 64 consecutive
+ * values x of one token and head:
+ *   z = f16(min x),  s = f16((max x - min x) / 15),  both clamped to +-65504
+ *   c = clip(rint((x - z) / s), 0, 15), or 0 where s = 0
+ *   value = z + s c
+ * in IEEE fp32 steps (difference, one division, round half to even), so 4.5
+ * bits a value with its scales.
+ * Layout: [page][head][block], a block holding 32 consecutive tokens in
+ * 32 D + 256 D/64 bytes (D = head_dim), with tile = t / 16, g = t % 16 / 4 for
+ * token t of the block and B(i) = 0, 2, 1, 3 for i = 0..3:
+ *   K codes: value 64 r + 8 h + j (h, j in 0..7) of token t sits in the low
+ *     (h < 4) or high nibble of byte
+ *       ((h%4 * 16 + t%16) * 2 + tile) * 8 + j/4 * 4 + B(j%4)          D = 64
+ *       ((tile * 4 + h%4) * 16 + t%16) * 16 + 8 r + j/4 * 4 + B(j%4)   D = 128
+ *   V codes: values 32 p + e and 32 p + 16 + e (e in 0..15) of token t are the
+ *     low and high nibble of byte
+ *       16 D + p/2 * 1024 + (g * 16 + e) * 16 + p%2 * 8 + tile * 4 + B(t%4)
+ *   scales: fp16 at 32 D + 256 r + 64 w + 16 g + 8 tile + 2 (t%4), w = 0..3:
+ *     K scale, K zero, V scale, V zero of token t, values 64 r .. 64 r + 63
+ * so that the bytes an attention lane loads are matrix operands as they lie. */
+typedef struct {
+  void* data;         /* DEVICE, 16-byte aligned, sherry_kv4_bytes(...) bytes */
+  int64_t n_pages;
+  int32_t page_size;  /* tokens per page: 32, 64, 128 or 256 */
+  int32_t n_kv_heads;
+  int32_t head_dim;   /* 64 or 128 */
+} sherry_kv4_cache;
+
+/* Bytes of such a cache; 0 for a shape it cannot have or on overflow. */
+size_t sherry_kv4_bytes(int64_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim);
+
+/* Quantise n tokens' keys and values into the cache.
+ *   k, v  : n tokens x n_kv_heads of dt (F32|F16|BF16)
+ *   slots : n int64, slot = page * page_size + place; a token whose slot is
+ *           negative or past the last page is skipped.  Slots of one call must
+ *           differ: of two tokens with the same slot, which one's codes and
+ *           scales stay is unspecified, per byte.
+ * Other tokens of the cache keep every bit.  Non-finite values are a caller
+ * error (the token's stored values are then unspecified).
+ * Errors: EINVAL null pointer, n < 0, bad cache counts; EDTYPE; ESHAPE
+ * page_size, head_dim, negative stride, size overflow; EALIGN. */
+sherry_status sherry_kv4_write(const sherry_kv4_cache* cache /* HOST */, const void* k, const void* v, sherry_dtype dt,
+                               int64_t n, int64_t k_stride_token, int64_t k_stride_head, int64_t v_stride_token,
+                               int64_t v_stride_head, const int64_t* slots, hipStream_t stream);
+
+/* Read n tokens back: value = z + s c in fp32, rounded once to dt.  Arguments as
+ * sherry_kv4_write, with k and v the outputs; a token whose slot is negative or
+ * past the last page reads as zeros, and slots may repeat. */
+sherry_status sherry_kv4_read(const sherry_kv4_cache* cache /* HOST */, void* k, void* v, sherry_dtype dt, int64_t n,
+                              int64_t k_stride_token, int64_t k_stride_head, int64_t v_stride_token,
+                              int64_t v_stride_head, const int64_t* slots, hipStream_t stream);
+
+/* Workspace bytes of sherry_kv4_attn with these arguments (0: none needed, or
+ * arguments that it refuses). */
+size_t sherry_kv4_attn_workspace(const sherry_kv4_cache* cache /* HOST */, int64_t n_tokens, int32_t n_q_heads,
+                                 int32_t n_seqs, int32_t max_q, int64_t max_kv);
+
+/* Causal attention of each sequence's new tokens over its cached ones (the new
+ * ones are written first, with sherry_kv4_write).  Token i of the n new tokens
+ * of a sequence with L cached tokens sees cached tokens 0 .. L - n + i:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
+ * A row that sees nothing (L < n - i) gives zeros, and -inf in lse.  Statistics
+ * and sums are fp32; the weights and V enter the matrix cores as fp16.
+ *   q, out     : n_tokens x n_q_heads of dt (F16|BF16); query head h reads key
+ *                head h / (n_q_heads / n_kv_heads)
+ *   cu_q       : n_seqs + 1 int32, ascending: sequence s has tokens cu_q[s] ..
+ *                cu_q[s + 1] - 1 (clamped to n_tokens; rows outside every
+ *                sequence are left as they were).  NULL: max_q tokens each,
+ *                n_tokens = n_seqs * max_q.
+ *   max_q      : at least the longest sequence's new tokens (of a longer one,
+ *                only the first max_q rows are computed)
+ *   max_kv     : the longest sequence's cached tokens, for sizing the launch
+ *                only; any value gives the same answer up to rounding
+ *   page_table : n_seqs rows of table_width int32 page numbers, row stride
+ *                table_stride (0: one row for all); tokens of an entry outside [0, n_pages) are not
+ *                seen, entries past a sequence's length not read
+ *   kv_lens    : n_seqs int32, L of each (clamped to 0 .. table_width *
+ *                page_size, which is at most 2^30)
+ *   lse        : n_tokens x n_q_heads fp32, or NULL
+ *   workspace  : sherry_kv4_attn_workspace(...) bytes, 16-byte aligned, of any
+ *                content, for this call alone: calls that may overlap (other
+ *                streams, graphs) need one each
+ * Results repeat bit for bit.  Errors: EINVAL null pointer or a count out of
+ * range; EDTYPE; ESHAPE head counts that do not divide, n_tokens against max_q
+ * without cu_q, negative stride, sizes past the launch's reach, a workspace
+ * that is too small; EALIGN. */
+sherry_status sherry_kv4_attn(const sherry_kv4_cache* cache /* HOST */, const void* q, sherry_dtype dt,
+                              int64_t n_tokens, int32_t n_q_heads, int64_t q_stride_token, int64_t q_stride_head,
+                              const int32_t* cu_q, int32_t n_seqs, int32_t max_q, int64_t max_kv,
+                              const int32_t* page_table, int32_t table_width, int64_t table_stride,
+                              const int32_t* kv_lens, float scale, void* out, int64_t out_stride_token,
+                              int64_t out_stride_head, float* lse, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
 /* ---- 2-bit dense-ternary comparator (Sherry Abstract and Figure 2: the
  * 2-bit aligned packing that keeps alignment by wasting bits) ----
  * Layout (a reading; the pages give none): 16 weights per little-endian

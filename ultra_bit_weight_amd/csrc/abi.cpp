@@ -452,6 +452,159 @@ sherry_status pack_impl(const void* w, dt_t w_dt, int64_t n, int64_t k, int64_t 
   return launched(launch_pack(w, w_dt, n, k, ldw, codes, scales, s_dt == SHERRY_F16, tern2, stream));
 }
 
+// ---- attention on the 4-bit cache ----
+
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+
+// Element type of an fp buffer, or -1.
+int act_dt(dt_t d) {
+  switch (d) {
+    case SHERRY_F32: return kActF32;
+    case SHERRY_F16: return kActF16;
+    case SHERRY_BF16: return kActBf16;
+    default: return -1;
+  }
+}
+
+// Strides of a [token][head][d] buffer: nothing negative, every offset in
+// 64 bits (n and heads are below 2^31, strides below 2^40 / heads).
+bool strides_fit(int64_t n, int64_t heads, int64_t st, int64_t sh) {
+  return st >= 0 && sh >= 0 && st <= kMaxStride && sh <= kMaxStride &&
+         n <= (std::numeric_limits<int64_t>::max() / 8) / std::max<int64_t>(1, st) &&
+         heads <= (std::numeric_limits<int64_t>::max() / 8) / std::max<int64_t>(1, sh);
+}
+
+// 16-byte rows.
+bool rows_aligned(const void* p, dt_t dt, int64_t st, int64_t sh) {
+  const int64_t e = static_cast<int64_t>(dt_size(dt));
+  return aligned(p, 16) && st * e % 16 == 0 && sh * e % 16 == 0;
+}
+
+sherry_status check_heads(const sherry_heads* h, dt_t x_dt, dt_t y_dt, int64_t n, int64_t d, RopeHeads* out) {
+  if (!h->x || !h->y || h->heads <= 0) return SHERRY_EINVAL;
+  if (h->heads > 65535 || !strides_fit(n, h->heads, h->x_stride_token, h->x_stride_head) ||
+      !strides_fit(n, h->heads, h->y_stride_token, h->y_stride_head) || (h->heads > 1 && h->y_stride_head < d) ||
+      (n > 1 && h->y_stride_token < d))
+    return SHERRY_ESHAPE;
+  if (!rows_aligned(h->x, x_dt, h->x_stride_token, h->x_stride_head) ||
+      !rows_aligned(h->y, y_dt, h->y_stride_token, h->y_stride_head) || (h->w && !aligned(h->w, 16)))
+    return SHERRY_EALIGN;
+  *out = RopeHeads{h->x, h->y, h->w, h->x_stride_token, h->x_stride_head, h->y_stride_token, h->y_stride_head, h->heads};
+  return SHERRY_OK;
+}
+
+size_t kv4_bytes_impl(int64_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim) {
+  if (n_pages <= 0 || n_kv_heads <= 0 || n_kv_heads > 65535) return 0;
+  if (page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256) return 0;
+  if (head_dim != 64 && head_dim != 128) return 0;
+  const int64_t page = static_cast<int64_t>(n_kv_heads) * (page_size / 32) * (32 * head_dim + 4 * head_dim);
+  if (n_pages > (int64_t(1) << 46) / page) return 0;
+  return static_cast<size_t>(n_pages * page);
+}
+
+sherry_status check_cache(const sherry_kv4_cache* c, Kv4Geom* out) {
+  if (!c || !c->data || c->n_pages <= 0 || c->n_kv_heads <= 0) return SHERRY_EINVAL;
+  if (kv4_bytes_impl(c->n_pages, c->page_size, c->n_kv_heads, c->head_dim) == 0) return SHERRY_ESHAPE;
+  if (!aligned(c->data, 16)) return SHERRY_EALIGN;
+  *out = Kv4Geom{static_cast<uint8_t*>(c->data), c->n_pages, __builtin_ctz(static_cast<unsigned>(c->page_size)),
+                 c->n_kv_heads};
+  return SHERRY_OK;
+}
+
+sherry_status kv4_rows_impl(const sherry_kv4_cache* cache, const void* k, const void* v, bool write, dt_t dt, int64_t n,
+                            int64_t k_st, int64_t k_sh, int64_t v_st, int64_t v_sh, const int64_t* slots,
+                            hipStream_t stream) {
+  Kv4Geom g;
+  if (n < 0) return SHERRY_EINVAL;
+  if (n == 0) return SHERRY_OK;
+  if (sherry_status s = check_cache(cache, &g)) return s;
+  if (!k || !v || !slots) return SHERRY_EINVAL;
+  if (act_dt(dt) < 0) return SHERRY_EDTYPE;
+  const int64_t heads = g.n_kv_heads, d = cache->head_dim;
+  if (n > kMaxDim || !strides_fit(n, heads, k_st, k_sh) || !strides_fit(n, heads, v_st, v_sh)) return SHERRY_ESHAPE;
+  if (!write && ((n > 1 && (k_st < d || v_st < d)) || (heads > 1 && (k_sh < d || v_sh < d)))) return SHERRY_ESHAPE;
+  if (n > kMaxDim / heads / (d / 8)) return SHERRY_ESHAPE;  // threads of the launch
+  if (!rows_aligned(k, dt, k_st, k_sh) || !rows_aligned(v, dt, v_st, v_sh) || !aligned(slots, 8)) return SHERRY_EALIGN;
+  if (sherry_status s = check_device()) return s;
+  Kv4Rows r{};
+  r.k = k;
+  r.v = v;
+  r.k_out = write ? nullptr : const_cast<void*>(k);
+  r.v_out = write ? nullptr : const_cast<void*>(v);
+  r.k_st = k_st;
+  r.k_sh = k_sh;
+  r.v_st = v_st;
+  r.v_sh = v_sh;
+  r.slots = slots;
+  r.n = n;
+  return launched(launch_kv4_rows(g, cache->head_dim, r, act_dt(dt), write, stream));
+}
+
+// Launch sizes of an attention call.
+sherry_status attn_sizes(const sherry_kv4_cache* cache, int64_t n_tokens, int32_t n_q_heads, int32_t n_seqs,
+                         int32_t max_q, int64_t max_kv, AttnArgs* a, size_t* workspace) {
+  if (max_q <= 0 || max_kv < 0 || n_q_heads <= 0) return SHERRY_EINVAL;
+  if (n_q_heads % a->c.n_kv_heads != 0 || n_q_heads > 65535 || n_tokens > kMaxDim) return SHERRY_ESHAPE;
+  a->n_tokens = n_tokens;
+  a->n_q_heads = n_q_heads;
+  a->n_seqs = n_seqs;
+  a->max_q = max_q;
+  a->group = n_q_heads / a->c.n_kv_heads;
+  const int64_t rows = static_cast<int64_t>(max_q) * a->group;
+  const int64_t tiles = (rows + kAttnRows - 1) / kAttnRows;
+  if (rows > kMaxDim / 256 || tiles * n_seqs > kMaxDim / 256) return SHERRY_ESHAPE;
+  a->row_tiles = static_cast<int32_t>(tiles);
+  a->splits = kv4_attn_splits(tiles * n_seqs * a->c.n_kv_heads, max_kv);
+  *workspace = a->splits == 1 ? 0 : static_cast<size_t>(a->splits) * n_tokens * n_q_heads * (cache->head_dim + 2) * 4;
+  return SHERRY_OK;
+}
+
+sherry_status kv4_attn_impl(const sherry_kv4_cache* cache, const void* q, dt_t dt, int64_t n_tokens, int32_t n_q_heads,
+                            int64_t q_st, int64_t q_sh, const int32_t* cu_q, int32_t n_seqs, int32_t max_q,
+                            int64_t max_kv, const int32_t* table, int32_t table_width, int64_t table_stride,
+                            const int32_t* kv_lens, float scale, void* out, int64_t o_st, int64_t o_sh, float* lse,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (n_tokens < 0 || n_seqs < 0) return SHERRY_EINVAL;
+  if (n_tokens == 0 || n_seqs == 0) return SHERRY_OK;
+  AttnArgs a{};
+  size_t need = 0;
+  if (sherry_status s = check_cache(cache, &a.c)) return s;
+  if (!q || !table || !kv_lens || !out || table_width <= 0) return SHERRY_EINVAL;
+  if (sherry_status s = attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, max_kv, &a, &need)) return s;
+  if (dt != SHERRY_F16 && dt != SHERRY_BF16) return SHERRY_EDTYPE;
+  const int64_t d = cache->head_dim;
+  if (!cu_q && n_tokens != static_cast<int64_t>(n_seqs) * max_q) return SHERRY_ESHAPE;
+  if (!strides_fit(n_tokens, n_q_heads, q_st, q_sh) || !strides_fit(n_tokens, n_q_heads, o_st, o_sh) ||
+      (n_tokens > 1 && o_st < d) || (n_q_heads > 1 && o_sh < d))
+    return SHERRY_ESHAPE;
+  if (table_stride < 0 || table_stride > kMaxStride ||
+      static_cast<int64_t>(table_width) > (int64_t(1) << 30) / cache->page_size)
+    return SHERRY_ESHAPE;
+  if (need && !workspace) return SHERRY_EINVAL;
+  if (workspace_bytes < need) return SHERRY_ESHAPE;
+  if (!rows_aligned(q, dt, q_st, q_sh) || !rows_aligned(out, dt, o_st, o_sh) || !aligned(table, 4) ||
+      !aligned(kv_lens, 4) || (cu_q && !aligned(cu_q, 4)) || (lse && !aligned(lse, 4)) ||
+      (need && !aligned(workspace, 16)))
+    return SHERRY_EALIGN;
+  if (sherry_status s = check_device()) return s;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.cu_q = cu_q;
+  a.table = table;
+  a.kv_lens = kv_lens;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + static_cast<int64_t>(a.splits) * n_tokens * n_q_heads * d;
+  a.q_st = q_st;
+  a.q_sh = q_sh;
+  a.o_st = o_st;
+  a.o_sh = o_sh;
+  a.table_stride = table_stride;
+  a.table_width = table_width;
+  a.scale = scale;
+  return launched(launch_kv4_attn(a, cache->head_dim, act_dt(dt), stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -675,6 +828,75 @@ sherry_status tern2_gemm(const uint32_t* codes, const void* w_scales, sherry_dty
                          int32_t* acc, void* y, sherry_dtype y_dt, int64_t ldy, hipStream_t stream) {
   return gemm_impl(kFmtTern2, codes, w_scales, raw(s_dt), n, k, x, raw(x_dt),
                    m, ldx, x_scales, acc, y, raw(y_dt), ldy, stream);
+}
+
+sherry_status sherry_qk_norm_rope(const sherry_heads* q, const sherry_heads* k, sherry_dtype x_dt, sherry_dtype y_dt,
+                                  int64_t n, int32_t head_dim, int32_t rot_dim, int32_t interleaved, const float* cos,
+                                  const float* sin, int64_t max_pos, const int64_t* positions, float eps,
+                                  hipStream_t stream) {
+  if (n < 0) return SHERRY_EINVAL;
+  if (n == 0) return SHERRY_OK;
+  if (!q || !cos || !sin || !positions || max_pos <= 0 || head_dim <= 0 || rot_dim <= 0) return SHERRY_EINVAL;
+  if (act_dt(raw(x_dt)) < 0 || act_dt(raw(y_dt)) < 0) return SHERRY_EDTYPE;
+  if (head_dim % 16 != 0 || head_dim > 256 || rot_dim % 16 != 0 || rot_dim > head_dim || n > kMaxDim ||
+      max_pos > (int64_t(1) << 40))
+    return SHERRY_ESHAPE;
+  RopeArgs a{};
+  if (sherry_status s = check_heads(q, raw(x_dt), raw(y_dt), n, head_dim, &a.q)) return s;
+  if (k)
+    if (sherry_status s = check_heads(k, raw(x_dt), raw(y_dt), n, head_dim, &a.k)) return s;
+  while (16 << a.lph_shift < head_dim) ++a.lph_shift;
+  if (n > (kMaxDim >> a.lph_shift) / (a.q.heads + a.k.heads)) return SHERRY_ESHAPE;  // threads of the launch
+  if (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(positions, 8)) return SHERRY_EALIGN;
+  if (sherry_status s = check_device()) return s;
+  a.cos = cos;
+  a.sin = sin;
+  a.pos = positions;
+  a.n = n;
+  a.max_pos = max_pos;
+  a.d = head_dim;
+  a.rot = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.eps = eps;
+  return launched(launch_qk_norm_rope(a, act_dt(raw(x_dt)), act_dt(raw(y_dt)), stream));
+}
+
+size_t sherry_kv4_bytes(int64_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim) {
+  return kv4_bytes_impl(n_pages, page_size, n_kv_heads, head_dim);
+}
+
+sherry_status sherry_kv4_write(const sherry_kv4_cache* cache, const void* k, const void* v, sherry_dtype dt, int64_t n,
+                               int64_t k_stride_token, int64_t k_stride_head, int64_t v_stride_token,
+                               int64_t v_stride_head, const int64_t* slots, hipStream_t stream) {
+  return kv4_rows_impl(cache, k, v, true, raw(dt), n, k_stride_token, k_stride_head, v_stride_token, v_stride_head,
+                       slots, stream);
+}
+
+sherry_status sherry_kv4_read(const sherry_kv4_cache* cache, void* k, void* v, sherry_dtype dt, int64_t n,
+                              int64_t k_stride_token, int64_t k_stride_head, int64_t v_stride_token,
+                              int64_t v_stride_head, const int64_t* slots, hipStream_t stream) {
+  return kv4_rows_impl(cache, k, v, false, raw(dt), n, k_stride_token, k_stride_head, v_stride_token, v_stride_head,
+                       slots, stream);
+}
+
+size_t sherry_kv4_attn_workspace(const sherry_kv4_cache* cache, int64_t n_tokens, int32_t n_q_heads, int32_t n_seqs,
+                                 int32_t max_q, int64_t max_kv) {
+  AttnArgs a{};
+  size_t need = 0;
+  if (n_tokens <= 0 || n_seqs <= 0 || check_cache(cache, &a.c) != SHERRY_OK) return 0;
+  if (attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, max_kv, &a, &need) != SHERRY_OK) return 0;
+  return need;
+}
+
+sherry_status sherry_kv4_attn(const sherry_kv4_cache* cache, const void* q, sherry_dtype dt, int64_t n_tokens,
+                              int32_t n_q_heads, int64_t q_stride_token, int64_t q_stride_head, const int32_t* cu_q,
+                              int32_t n_seqs, int32_t max_q, int64_t max_kv, const int32_t* page_table,
+                              int32_t table_width, int64_t table_stride, const int32_t* kv_lens, float scale, void* out,
+                              int64_t out_stride_token, int64_t out_stride_head, float* lse, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+  return kv4_attn_impl(cache, q, raw(dt), n_tokens, n_q_heads, q_stride_token, q_stride_head, cu_q, n_seqs, max_q,
+                       max_kv, page_table, table_width, table_stride, kv_lens, scale, out, out_stride_token,
+                       out_stride_head, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

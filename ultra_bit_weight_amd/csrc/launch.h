@@ -241,4 +241,77 @@ hipError_t launch_tern3_encode(const int8_t* t, int64_t n, int64_t k, int64_t ld
 hipError_t launch_tern2_encode(const int8_t* t, int64_t n, int64_t k, int64_t ldt, uint32_t* codes,
                                hipStream_t stream);
 
+
+// Norms and rotation of query and key heads (rope.hip).  A head takes
+// 1 << lph_shift lanes of 16 values.
+struct RopeHeads {
+  const void* x;
+  void* y;
+  const float* w;  // nullable: no norm
+  int64_t x_st, x_sh, y_st, y_sh;
+  int32_t heads;
+};
+struct RopeArgs {
+  RopeHeads q, k;
+  const float* cos;
+  const float* sin;
+  const int64_t* pos;
+  int64_t n;
+  int64_t max_pos;
+  int32_t d;
+  int32_t rot;
+  int32_t interleaved;
+  int32_t lph_shift;
+  float eps;
+};
+hipError_t launch_qk_norm_rope(const RopeArgs& a, int xdt, int ydt, hipStream_t stream);
+
+// The 4-bit key/value cache (kv4.hip, kv4_attn.hip; layout in kv4.h).
+// Geometry of a cache as the kernels take it.
+struct Kv4Geom {
+  uint8_t* data;
+  int64_t n_pages;
+  int32_t page_shift;  // log2 of tokens per page
+  int32_t n_kv_heads;
+};
+struct Kv4Rows {
+  const void* k;
+  const void* v;
+  void* k_out;
+  void* v_out;
+  int64_t k_st, k_sh, v_st, v_sh;
+  const int64_t* slots;
+  int64_t n;
+};
+hipError_t launch_kv4_rows(const Kv4Geom& g, int head_dim, const Kv4Rows& r, int dt, bool write, hipStream_t stream);
+
+struct AttnArgs {
+  Kv4Geom c;
+  const void* q;
+  void* out;
+  float* lse;             // nullable
+  const int32_t* cu_q;    // nullable: max_q tokens of every sequence
+  const int32_t* table;
+  const int32_t* kv_lens;
+  float* part_o;          // splits x tokens x heads x D, when splits > 1
+  float* part_ml;         // the same x (maximum, sum)
+  int64_t q_st, q_sh, o_st, o_sh;
+  int64_t n_tokens;
+  int64_t table_stride;
+  int32_t table_width;
+  int32_t n_seqs;
+  int32_t n_q_heads;
+  int32_t group;          // query heads per key head
+  int32_t max_q;
+  int32_t splits;
+  int32_t row_tiles;      // 16-row tiles of max_q tokens x group
+  int32_t join_blocks;    // workgroups of the join per sequence
+  float scale;
+};
+// Rows (tokens x query heads of one key head) per tile, and the shares that a
+// sequence's cached tokens are split into.
+constexpr int kAttnRows = 16;
+int32_t kv4_attn_splits(int64_t workgroups, int64_t max_kv);
+hipError_t launch_kv4_attn(const AttnArgs& a, int head_dim, int dt, hipStream_t stream);
+
 }  // namespace sherry

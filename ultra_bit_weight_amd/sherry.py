@@ -31,6 +31,8 @@ EXPORTS = [
     "sherry_gemm_plan_bytes", "sherry_gemm_plan", "sherry_gemm_grouped",
     "tern2_packed_bytes", "tern2_pack", "tern2_encode", "tern2_gemv", "tern2_gemv_plan", "tern2_gemm", "tern2_gemm_plan",
     "tern3_packed_bytes", "tern3_encode", "tern3_gemv", "tern3_gemv_plan_bytes", "tern3_gemv_plan",
+    "sherry_qk_norm_rope", "sherry_kv4_bytes", "sherry_kv4_write", "sherry_kv4_read", "sherry_kv4_attn_workspace",
+    "sherry_kv4_attn",
     "sherry_probe_read", "sherry_probe_rates", "sherry_probe_clock", "sherry_set_prefill_kernel",
 ]
 
@@ -52,6 +54,17 @@ class GemmProblem(ctypes.Structure):
                 ("k", ctypes.c_int64), ("x", ctypes.c_void_p), ("m", ctypes.c_int64), ("ldx", ctypes.c_int64),
                 ("x_scales", ctypes.c_void_p), ("acc", ctypes.c_void_p), ("y", ctypes.c_void_p),
                 ("ldy", ctypes.c_int64)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                ("x_stride_token", ctypes.c_int64), ("x_stride_head", ctypes.c_int64),
+                ("y_stride_token", ctypes.c_int64), ("y_stride_head", ctypes.c_int64), ("heads", ctypes.c_int32)]
+
+
+class Kv4CacheDesc(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 _lib = None
@@ -121,6 +134,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         f.argtypes = [ctypes.POINTER(GemmProblem), i32, i, i, i, vp, sz]
     lib.sherry_gemm_grouped.restype = i
     lib.sherry_gemm_grouped.argtypes = [vp, vp, vp]
+    hp, cp, f = ctypes.POINTER(Heads), ctypes.POINTER(Kv4CacheDesc), ctypes.c_float
+    lib.sherry_qk_norm_rope.restype = i
+    lib.sherry_qk_norm_rope.argtypes = [hp, hp, i, i, i64, i32, i32, i32, vp, vp, i64, vp, f, vp]
+    lib.sherry_kv4_bytes.restype = sz
+    lib.sherry_kv4_bytes.argtypes = [i64, i32, i32, i32]
+    for f_rows in (lib.sherry_kv4_write, lib.sherry_kv4_read):
+        f_rows.restype = i
+        f_rows.argtypes = [cp, vp, vp, i, i64, i64, i64, i64, i64, vp, vp]
+    lib.sherry_kv4_attn_workspace.restype = sz
+    lib.sherry_kv4_attn_workspace.argtypes = [cp, i64, i32, i32, i32, i64]
+    lib.sherry_kv4_attn.restype = i
+    lib.sherry_kv4_attn.argtypes = [cp, vp, i, i64, i32, i64, i64, vp, i32, i32, i64, vp, i32, i64, vp, f, vp, i64, i64,
+                                    vp, vp, sz, vp]
     lib.sherry_set_prefill_kernel.restype = i
     lib.sherry_set_prefill_kernel.argtypes = [i]
     _lib = lib
@@ -548,3 +574,201 @@ class GroupedGemm:
 
     def __call__(self):
         _check("sherry_gemm_grouped", load().sherry_gemm_grouped(self.host.data_ptr(), self.dev.data_ptr(), _stream()))
+
+
+# ---- attention on a 4-bit key/value cache ----
+
+_FP = (torch.float32, torch.float16, torch.bfloat16)
+
+
+def _same_gpu(dev, **named):
+    for name, t in named.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on the GPU")
+
+
+def _launch(fn_name, f, dev, *args):
+    """The call on the tensors' own device and its current stream, whichever
+    device is current."""
+    if dev.index == torch.cuda.current_device():
+        status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status:
+        _check(fn_name, status)
+
+
+def _check_heads_tensor(t, name, shape=None, dtypes=_FP):
+    """[tokens, heads, head_dim] with unit stride along head_dim."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with unit stride along head_dim")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {[str(d) for d in dtypes]}")
+
+
+def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out_dtype=None,
+                 q_out=None, k_out=None):
+    """RMS norm of each query and key head (with q_weight / k_weight, fp32
+    [head_dim]; without one that side is not normalised) and the rotation of
+    its position, in one launch (sherry_qk_norm_rope).
+
+    q [n, heads, d] and k [n, kv_heads, d] or None (fp32, fp16 or bf16, any
+    token and head strides: slices of a fused q|k|v output are taken as they
+    lie); cos, sin fp32 [max_pos, rot_dim / 2]; positions int64 [n].  The first
+    rot_dim values rotate as pairs (i, i + rot_dim / 2), or (2i, 2i + 1) with
+    interleaved.  q_out / k_out may be q / k themselves.  Returns (q, k)."""
+    _check_heads_tensor(q, "q")
+    n, hq, d = q.shape
+    if k is not None:
+        _check_heads_tensor(k, "k", (n, k.shape[1] if k.dim() == 3 else 0, d), (q.dtype,))
+    _need(cos, "cos", dim=2, dtypes=(torch.float32,))
+    _need(sin, "sin", dim=2, dtypes=(torch.float32,))
+    if cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous():
+        raise ValueError("cos and sin must be contiguous and of one shape [max_pos, rot_dim / 2]")
+    _need(positions, "positions", numel=n, dim=1, dtypes=(torch.int64,))
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _need(w, name, numel=d, dim=1, dtypes=(torch.float32,))
+        if w is not None and not w.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if not positions.is_contiguous():
+        raise ValueError("positions must be contiguous")
+    y_dt = out_dtype or (q_out.dtype if q_out is not None else q.dtype)
+    if q_out is None:
+        q_out = torch.empty(n, hq, d, dtype=y_dt, device=q.device)
+    _check_heads_tensor(q_out, "q_out", q.shape, (y_dt,) if y_dt in _FP else _FP)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=y_dt, device=q.device)
+        _check_heads_tensor(k_out, "k_out", k.shape, (y_dt,))
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    _same_gpu(q.device, k=k, cos=cos, sin=sin, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
+              k_out=k_out)
+    qs = Heads(q.data_ptr(), q_out.data_ptr(), _ptr(q_weight), q.stride(0), q.stride(1), q_out.stride(0),
+               q_out.stride(1), hq)
+    ks = None
+    if k is not None:
+        ks = Heads(k.data_ptr(), k_out.data_ptr(), _ptr(k_weight), k.stride(0), k.stride(1), k_out.stride(0),
+                   k_out.stride(1), k.shape[1])
+    _launch("sherry_qk_norm_rope", load().sherry_qk_norm_rope, q.device, qs, ks, _DT[q.dtype], _DT[y_dt], n, d,
+            2 * cos.shape[1], int(bool(interleaved)), cos.data_ptr(), sin.data_ptr(), cos.shape[0],
+            positions.data_ptr(), eps)
+    return q_out, k_out
+
+
+class Kv4Cache:
+    """A paged key/value cache in 4 bits (sherry_kv4_cache): n_pages pages of
+    page_size tokens (32, 64, 128 or 256), n_kv_heads heads of head_dim 64 or
+    128.  `data` holds it (uint8, zeroed; pass one to use memory of your own)."""
+
+    def __init__(self, n_pages, page_size, n_kv_heads, head_dim, device=None, data=None):
+        nbytes = load().sherry_kv4_bytes(n_pages, page_size, n_kv_heads, head_dim)
+        if nbytes == 0:
+            raise ValueError(f"no cache of {n_pages} pages of {page_size} tokens, {n_kv_heads} heads of {head_dim}")
+        if data is None:
+            data = torch.zeros(nbytes, dtype=torch.uint8, device=device or "cuda")
+        _need(data, "data", dtypes=(torch.uint8,), min_nbytes=nbytes)
+        if not data.is_contiguous():
+            raise ValueError("data must be contiguous")
+        self.data, self.nbytes = data, nbytes
+        self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
+        self.desc = Kv4CacheDesc(data.data_ptr(), n_pages, page_size, n_kv_heads, head_dim)
+
+
+def _check_slots(slots):
+    _need(slots, "slots", dim=1, dtypes=(torch.int64,))
+    if not slots.is_contiguous():
+        raise ValueError("slots must be contiguous")
+    return slots.numel()
+
+
+def kv4_write(cache, k, v, slots):
+    """Quantise k, v [n, kv_heads, head_dim] (fp32, fp16 or bf16, any token and
+    head strides) into the cache at slots (int64 [n], page * page_size + place,
+    all different; one outside the cache is skipped) (sherry_kv4_write)."""
+    shape = (_check_slots(slots), cache.n_kv_heads, cache.head_dim)
+    _check_heads_tensor(k, "k", shape)
+    _check_heads_tensor(v, "v", shape, (k.dtype,))
+    _same_gpu(cache.data.device, k=k, v=v, slots=slots)
+    _launch("sherry_kv4_write", load().sherry_kv4_write, cache.data.device, cache.desc, k.data_ptr(), v.data_ptr(),
+            _DT[k.dtype], shape[0], k.stride(0), k.stride(1), v.stride(0), v.stride(1), slots.data_ptr())
+
+
+def kv4_read(cache, slots, out_dtype=torch.float16, k_out=None, v_out=None):
+    """The values that the cache holds at slots (int64 [n]) as k, v
+    [n, kv_heads, head_dim]; slots outside the cache read as zeros
+    (sherry_kv4_read)."""
+    shape = (_check_slots(slots), cache.n_kv_heads, cache.head_dim)
+    if k_out is not None or v_out is not None:
+        out_dtype = (k_out if k_out is not None else v_out).dtype
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=out_dtype, device=cache.data.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=out_dtype, device=cache.data.device)
+    _check_heads_tensor(k_out, "k_out", shape)
+    _check_heads_tensor(v_out, "v_out", shape, (k_out.dtype,))
+    _same_gpu(cache.data.device, slots=slots, k_out=k_out, v_out=v_out)
+    _launch("sherry_kv4_read", load().sherry_kv4_read, cache.data.device, cache.desc, k_out.data_ptr(),
+            v_out.data_ptr(), _DT[k_out.dtype], shape[0], k_out.stride(0), k_out.stride(1), v_out.stride(0),
+            v_out.stride(1), slots.data_ptr())
+    return k_out, v_out
+
+
+def kv4_attn_workspace(cache, n_tokens, n_q_heads, n_seqs, max_q=1, max_kv=0):
+    """A workspace for kv4_attn calls of these sizes (sherry_kv4_attn_workspace);
+    calls that may run at the same time need one each."""
+    nbytes = load().sherry_kv4_attn_workspace(cache.desc, n_tokens, n_q_heads, n_seqs, max_q, max_kv)
+    return torch.empty(nbytes, dtype=torch.uint8, device=cache.data.device)
+
+
+def kv4_attn(cache, q, page_table, kv_lens, cu_q=None, max_q=1, max_kv=None, scale=None, out=None, lse=None,
+             want_lse=False, workspace=None):
+    """Causal attention of new tokens q [n, heads, head_dim] (fp16 or bf16) over
+    the cache (sherry_kv4_attn): sequence s has the tokens cu_q[s] ..
+    cu_q[s + 1] - 1 (int32 [n_seqs + 1]; without it max_q tokens each), its
+    cached tokens (the new ones included) lie in the pages page_table[s]
+    (int32 [n_seqs, width]), and kv_lens[s] (int32) counts them.  max_q bounds
+    the new tokens of a sequence, max_kv (default: what the table holds) sizes
+    the launch, scale defaults to head_dim ** -0.5.  A row that sees nothing is
+    zeros.  Returns (out, lse fp32 [n, heads] or None)."""
+    _check_heads_tensor(q, "q", dtypes=(torch.float16, torch.bfloat16))
+    n, hq, d = q.shape
+    if d != cache.head_dim:
+        raise ValueError(f"q has head_dim {d}, the cache {cache.head_dim}")
+    _need(page_table, "page_table", dim=2, dtypes=(torch.int32,))
+    n_seqs, width = page_table.shape
+    if width > 1 and page_table.stride(1) != 1:
+        raise ValueError("page_table must have unit stride along its rows")
+    _need(kv_lens, "kv_lens", numel=n_seqs, dim=1, dtypes=(torch.int32,))
+    _need(cu_q, "cu_q", numel=n_seqs + 1, dim=1, dtypes=(torch.int32,))
+    if not kv_lens.is_contiguous() or (cu_q is not None and not cu_q.is_contiguous()):
+        raise ValueError("kv_lens and cu_q must be contiguous")
+    if out is None:
+        out = torch.empty(n, hq, d, dtype=q.dtype, device=q.device)
+    _check_heads_tensor(out, "out", q.shape, (q.dtype,))
+    if lse is None and want_lse:
+        lse = torch.empty(n, hq, dtype=torch.float32, device=q.device)
+    _need(lse, "lse", dim=2, dtypes=(torch.float32,))
+    if lse is not None and (tuple(lse.shape) != (n, hq) or not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous [{n}, {hq}], got shape {tuple(lse.shape)}")
+    if max_kv is None:
+        max_kv = width * cache.page_size
+    if workspace is None:
+        workspace = kv4_attn_workspace(cache, n, hq, n_seqs, max_q, max_kv)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _same_gpu(cache.data.device, q=q, page_table=page_table, kv_lens=kv_lens, cu_q=cu_q, out=out, lse=lse,
+              workspace=workspace)
+    _launch("sherry_kv4_attn", load().sherry_kv4_attn, q.device, cache.desc, q.data_ptr(), _DT[q.dtype], n, hq,
+            q.stride(0), q.stride(1), _ptr(cu_q), n_seqs, max_q, max_kv, page_table.data_ptr(), width,
+            page_table.stride(0), kv_lens.data_ptr(), scale if scale is not None else d ** -0.5,
+            out.data_ptr(), out.stride(0), out.stride(1), _ptr(lse), workspace.data_ptr() or None,
+            workspace.numel() * workspace.element_size())
+    return out, lse
