@@ -93,10 +93,12 @@ def norm_rope(x, w, cos, sin, eps, rot, interleaved):
     return y
 
 
-def attention(q, k, v, scale):
+def attention(q, k, v, scale, vmag=None):
     """One sequence: q [n, hq, d], k and v [L, hkv, d] -> out fp64 [n, hq, d],
-    lse [n, hq], and sum_j w_j |v_j| [n, hq, d] (what errors scale with)."""
+    lse [n, hq], and sum_j w_j vmag_j [n, hq, d] (vmag: |v| unless given; what
+    errors of the terms scale with)."""
     q, k, v = (np.asarray(a, np.float64) for a in (q, k, v))
+    vmag = np.abs(v) if vmag is None else vmag
     n, hq, d = q.shape
     length, hkv = k.shape[:2]
     out, mag = np.zeros((n, hq, d)), np.zeros((n, hq, d))
@@ -112,5 +114,5 @@ def attention(q, k, v, scale):
             e = np.exp(s - m)
             lse[i, h] = m + np.log(e.sum())
             out[i, h] = e @ v[:seen, kh] / e.sum()
-            mag[i, h] = e @ np.abs(v[:seen, kh]) / e.sum()
+            mag[i, h] = e @ vmag[:seen, kh] / e.sum()
     return out, lse, mag

@@ -5,10 +5,11 @@ Tolerances, from the number formats (half a step: fp16 2^-11, bf16 2^-8, fp32
   cache: codes and scales bit for bit; values read back one fp32 step and one
     rounding to the output type.
   rotation: fp32 throughout; see rope_tolerance().
-  attention: V and the weights enter the product as fp16, so each term w |v| is
-    off by at most 2 * 2^-11 of itself; a score (in natural units) is off by
-    at most `ds`, which moves a weight by the factor e^(+-2 ds); the result is
-    rounded once.  See attn_tolerance().
+  attention: the weights enter the product as fp16 P = p s, beside the exact
+    codes: each term is off by at most 2^-11 of p s |c - mid|, |c - mid| <=
+    |c - 7.5| + 0.5.  A score (in natural units) is off by at most `ds`, which
+    moves a weight by the factor e^(+-2 ds).  The result is rounded once.  See
+    attn_reference().
 """
 import numpy as np
 import pytest
@@ -244,16 +245,32 @@ def test_kv4_extreme_values(gpu_lib):
 
 # ------------------------------------------------------------- attention ---
 
-def attn_tolerance(q, k, mag, out, scale, dtype):
-    """Elementwise bound on |out - exact| and the bound on lse.  A score is a sum
-    over d of q (z + s c) taken as s (q . c) + z sum(q): D terms, each product of
-    q with a code (up to 15 s) or z exact or one step, added in fp32 in an order
-    of their own: at most D + 8 half steps of the sum of magnitudes, here
-    15 s + |z| <= 3 max |k| of the key's group."""
+def stored(x):
+    """What the cache holds of x: values, and per value s (|c - 7.5| + 0.5) and
+    23 s + |z|."""
+    c, sc, z = attn_ref.quantise(host(x))
+    g = c.shape[:-1] + (c.shape[-1] // 64, 64)
+    s64 = np.broadcast_to(sc.astype(np.float64)[..., None], g)
+    z64 = np.broadcast_to(np.abs(z.astype(np.float64))[..., None], g)
+    return (attn_ref.dequantise(c, sc, z), (s64 * (np.abs(c.reshape(g) - 7.5) + 0.5)).reshape(c.shape),
+            (23 * s64 + z64).reshape(c.shape))
+
+
+def attn_reference(q, k, v, scale, dtype):
+    """out, lse and their bounds; k and v from stored().
+
+    A score is a sum over d of q (z + s c) taken as s (q . c) + z sum(q): D terms
+    of q times a code (up to 15 s) or z, exact or one step each, added in fp32 in
+    an order of their own: at most D + 8 half steps of the sum of magnitudes,
+    15 s + |z| <= 3 max |k|.  The terms of the result, p s c (c <= 15) and
+    p (z + mid s) (mid <= 8), are added in fp32, 32 tokens at a time and in up to
+    64 shares: at most L / 32 + 64 half steps of p (23 s + |z|)."""
     d = q.shape[-1]
-    ds = (d + 8) * 2.0 ** -24 * scale * np.abs(q).sum(-1).max() * 3 * np.abs(k).max() if k.size and q.size else 0.0
-    tol = mag * (2 * 2.0 ** -11 + 2 * ds + 2.0 ** -18) + np.abs(out) * HALF[dtype] + TINY[dtype]
-    return tol * (1 + 2.0 ** -8), ds + 2.0 ** -20
+    kd, (vd, vround, vsum) = k[0], v
+    ds = (d + 8) * 2.0 ** -24 * scale * np.abs(q).sum(-1).max() * 3 * np.abs(kd).max() if kd.size and q.size else 0.0
+    vmag = 2.0 ** -11 * vround + 2.0 ** -24 * (len(kd) / 32 + 64) * vsum + 2 * ds * np.abs(vd)
+    ref, lse, mag = attn_ref.attention(q, kd, vd, scale, vmag)
+    return ref, (mag + np.abs(ref) * HALF[dtype] + TINY[dtype]) * (1 + 2.0 ** -8), lse, ds + 2.0 ** -20
 
 
 class Batch:
@@ -279,8 +296,8 @@ class Batch:
         self.scale = d ** -0.5
         for i, length in enumerate(ls):
             k, v = make_kv(length, hkv, d, dtype, seed + 10 * i + 1) if length else (torch.zeros(0, hkv, d),) * 2
-            self.kd.append(attn_ref.dequantise(*attn_ref.quantise(host(k))))
-            self.vd.append(attn_ref.dequantise(*attn_ref.quantise(host(v))))
+            self.kd.append(stored(k))
+            self.vd.append(stored(v))
             j = np.arange(length)
             slots = table[i, j // page_size].astype(np.int64) * page_size + j % page_size
             if length:
@@ -299,8 +316,7 @@ class Batch:
         for i, n in enumerate(self.qs):
             if seqs is None or i in seqs:
                 q = host(self.q[at:at + n]).astype(np.float64)
-                ref, rl, mag = attn_ref.attention(q, self.kd[i], self.vd[i], self.scale)
-                tol, ltol = attn_tolerance(q, self.kd[i], mag, ref, self.scale, self.dtype)
+                ref, tol, rl, ltol = attn_reference(q, self.kd[i], self.vd[i], self.scale, self.dtype)
                 got = host(out[at:at + n]).astype(np.float64)
                 err = np.abs(got - ref)
                 assert (err <= tol).all(), (i, np.nanmax(err - tol), np.isnan(got).sum())
@@ -407,8 +423,8 @@ def test_attn_bad_tables_and_lengths(gpu_lib):
     b.check(out, lse, seqs=[0])
     for s, keep in ((1, np.r_[0:32, 64:96]), (2, np.r_[32:96])):
         q = host(b.q[s:s + 1]).astype(np.float64)
-        ref, _, mag = attn_ref.attention(q, b.kd[s][keep], b.vd[s][keep], b.scale)
-        tol, _ = attn_tolerance(q, b.kd[s], mag, ref, b.scale, b.dtype)
+        kept = [[a[keep] for a in x] for x in (b.kd[s], b.vd[s])]
+        ref, tol, _, _ = attn_reference(q, *kept, b.scale, b.dtype)
         assert (np.abs(host(out[s:s + 1]).astype(np.float64) - ref) <= tol).all()
     assert not out[3].any() and torch.isneginf(lse[3]).all()
     cu = torch.tensor([0, 1, 2, 3, 99], dtype=torch.int32, device=DEV)
@@ -443,7 +459,7 @@ def test_attn_sink(gpu_lib):
         k[where] = 1.0
         v = randn(4096, 1, 64, seed=1001)
         b.q = torch.full((1, 4, 64), 1.4, dtype=torch.float16)
-        b.kd, b.vd = ([attn_ref.dequantise(*attn_ref.quantise(x.numpy()))] for x in (k, v))
+        b.kd, b.vd = [stored(k)], [stored(v)]
         j = torch.arange(4096, device=DEV)
         slots = b.table[0].long()[j // 64] * 64 + j % 64
         b.lib.kv4_write(b.cache, k.to(DEV), v.to(DEV), slots)
@@ -477,12 +493,11 @@ def test_attn_far_pages(gpu_lib):
     slots = table[0].long()[j // page] * page + j % page
     gpu_lib.kv4_write(cache, k.to(DEV), v.to(DEV), slots)
     rk, _ = gpu_lib.kv4_read(cache, slots, out_dtype=torch.float32)
-    kd, vd = (attn_ref.dequantise(*attn_ref.quantise(host(x))) for x in (k, v))
-    assert np.abs(host(rk) - kd).max() <= np.abs(kd).max() * 2.0 ** -23
+    kd, vd = stored(k), stored(v)
+    assert np.abs(host(rk) - kd[0]).max() <= np.abs(kd[0]).max() * 2.0 ** -23
     q = randn(2, 16, d, seed=1201, dtype=torch.float16)
     out, _ = gpu_lib.kv4_attn(cache, q.to(DEV), table, torch.tensor([300], dtype=torch.int32, device=DEV), max_q=2)
-    ref, _, mag = attn_ref.attention(host(q), kd, vd, d ** -0.5)
-    tol, _ = attn_tolerance(host(q).astype(np.float64), kd, mag, ref, d ** -0.5, torch.float16)
+    ref, tol, _, _ = attn_reference(host(q).astype(np.float64), kd, vd, d ** -0.5, torch.float16)
     assert (np.abs(host(out) - ref) <= tol).all()
 
 
@@ -535,12 +550,11 @@ def test_decode_layer_together(gpu_lib):
         tol = rope_tolerance(f[:, :hq], host(w["nq"]), host(cos)[[t]], host(sin)[[t]], 1e-6, d, False, torch.float16)
         ref = attn_ref.norm_rope(f[:, :hq], host(w["nq"]), host(cos)[[t]], host(sin)[[t]], 1e-6, d, False)
         assert (np.abs(host(q) - ref) <= tol).all()
-        ks.append(attn_ref.dequantise(*attn_ref.quantise(host(k)[0])))
-        vs.append(attn_ref.dequantise(*attn_ref.quantise(f[0, hq + hkv:])))
+        ks.append(stored(k))
+        vs.append([a[None] for a in stored(torch.from_numpy(f[0, hq + hkv:].copy()))])
         if t in (0, 1, 31, 32, 63, 64, 69):
-            kd, vd = np.stack(ks), np.stack(vs)
-            ref, _, mag = attn_ref.attention(host(q), kd, vd, d ** -0.5)
-            tol, _ = attn_tolerance(host(q).astype(np.float64), kd, mag, ref, d ** -0.5, torch.float16)
+            kd, vd = ([np.concatenate(a) for a in zip(*x)] for x in (ks, vs))
+            ref, tol, _, _ = attn_reference(host(q).astype(np.float64), kd, vd, d ** -0.5, torch.float16)
             assert (np.abs(host(att) - ref) <= tol).all()
             oo = gpu_lib.gemv_quant(*w["o"], att.view(-1))[1]
             assert torch.equal(oo, o)

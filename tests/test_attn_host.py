@@ -71,7 +71,7 @@ def test_kv4_rows_refusals(lib, fn):  # noqa: F811
     assert f(kt=0) == expect and f(vh=0) == expect
 
 
-def attn(lib, c=0, q=A, dt=F16, n=4, hq=32, qt=2048, qh=64, cu=A, seqs=4, max_q=1, max_kv=1000, table=A, width=16,
+def attn(lib, c=0, q=A, dt=F16, n=4, hq=32, qt=2048, qh=64, cu=A, seqs=4, max_q=1, max_kv=100000, table=A, width=16,
          stride=16, lens=A, scale=0.125, out=A, ot=2048, oh=64, lse=A, ws=A, ws_bytes=2 ** 30):
     return lib.sherry_kv4_attn(cache() if c == 0 else c, q, dt, n, hq, qt, qh, cu, seqs, max_q, max_kv, table, width,
                                stride, lens, scale, out, ot, oh, lse, ws, ws_bytes, None)

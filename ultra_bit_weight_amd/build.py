@@ -45,7 +45,10 @@ def common_flags() -> list:
 # VGPRs (the default AGPR form made the compiler copy the tiled kernel's
 # accumulators between the two register files on every k step, and the rate
 # probe's 4 products per iteration came with 20 such copies).
-FILE_FLAGS = {"gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+# kv4_attn.hip: the same, its accumulators are rescaled and its operands made
+# in ordinary VGPRs.
+FILE_FLAGS = {"kv4_attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+              "gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
               "probes.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 

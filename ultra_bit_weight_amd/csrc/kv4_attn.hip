@@ -2,8 +2,8 @@
 //
 //   o_i = sum_j softmax_j(scale q_i . k_j) v_j,  j <= position of i
 //
-// One pass over the cache with a running maximum and sum.  A wave takes 16
-// rows (tokens x query heads of one key head) and blocks of 32 cached tokens:
+// One pass over the cache with a running maximum and sum, on blocks of 32
+// cached tokens and tiles of 16 rows (tokens x query heads of one key head):
 //
 //   S^T [32 tokens x 16 rows] = K Q^T     v_mfma_f32_16x16x32_f16
 //   O^T [D x 16 rows]        += V^T P^T   the same instruction
@@ -12,14 +12,23 @@
 // are its P^T operand as they stand: the layout of V numbers the tokens of the
 // product's reduction axis the way the first product leaves them.
 //
-// K codes enter the product as fp16 subnormals (code c at bits 0-3 is c 2^-24,
-// at bits 4-7 c 2^-20; the queries of those products are scaled by 2^-4), so
-// unpacking costs a mask per two codes; with codes c and queries q
-//   q . k_j = s_j (q . c_j) + z_j sum(q)      per 64 values
-// restores scale and zero point in fp32.  q is scaled to fp16 by a power of two
-// per row, exactly for both input types.  V is restored to fp16 in registers
-// (1024 + c, - 1024, * s + z: one rounding), so that one P serves all groups.
+// Scale and zero point stay outside the products, whose operands are the codes
+// themselves (exact in fp16) on one side.  Per 64 values, with codes c:
+//   q . k_j = s_j (q . c_j) + z_j sum(q)
+//   sum_j p_j v_j = sum_j P_j (c_j - mid) + sum_j p_j (z_j + mid s_j),  P = p s
+// So K enters without rounding, q is brought to fp16 by a power of two (exact
+// for both input types), and the one rounding inside is P to fp16: 2^-11 of
+// each term at most, like the result's own.  mid = 8 centres V's codes: sums of
+// 0..15 would cancel against the zero point's part to a result that over a long
+// axis is hundreds of times smaller (0.0006 instead of 0.0003 of it lost at
+// 131072 tokens).
+//
+// Unpacking: a code at bits 0-3 of a half is the fp16 subnormal c 2^-24, at
+// bits 4-7 c 2^-20, so for K a mask makes two operands of a dword's eight (the
+// shift by 8 brings the others) and the power of two is taken off the queries;
+// for V a packed addition of -8 follows, and the power of two is taken off O.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4.h"
 
@@ -30,53 +39,41 @@ constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * kWave;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// P is held times 2^7 (fp16 keeps 2^-14 .. 65504: weights down to 2^-21 of the
-// running maximum in full precision), and the running maximum is only raised
-// when a score exceeds it by 2^8: P <= 2^15.
+// The running maximum is one of score + log2(V scale), so that P's largest is
+// 2^kPExp when it is set; it is raised again only when some P passes kPTop
+// (fp16 ends at 65504).  P keeps full precision down to 2^-21 of the largest.
+// A V scale of 0 (a constant group, a token never written) hides p from P: it
+// counts as 2^-24 for the maximum, and the sum of p is watched too.
 constexpr float kPExp = 7.0f;
-constexpr float kSlack = 8.0f;
+constexpr float kPTop = 32768.0f;
+constexpr float kSumTop = 1.0e18f;
 constexpr float kNoMax = -1.0e30f;
-
-template <int D>
-struct Stage {  // one block's operands, as loaded
-  u32x4_t k[D / 32], v[D / 64], ks[D / 64], kz[D / 64], vs[D / 64], vz[D / 64];
-};
-
-template <int D>
-__device__ __forceinline__ void load_block(const uint8_t* blk, int lane, Stage<D>& st) {
-  using L = Kv4Layout<D>;
-  const SHERRY_GLOBAL uint8_t* b = gmem(blk);
-  const int g = lane >> 4;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    st.k[i] = *reinterpret_cast<const SHERRY_GLOBAL u32x4_t*>(b + i * 1024 + lane * 16);
-    st.v[i] = *reinterpret_cast<const SHERRY_GLOBAL u32x4_t*>(b + L::kVOff + i * 1024 + lane * 16);
-    const SHERRY_GLOBAL u32x4_t* p = reinterpret_cast<const SHERRY_GLOBAL u32x4_t*>(b + L::kPOff + i * 256 + g * 16);
-    st.ks[i] = p[0], st.kz[i] = p[4], st.vs[i] = p[8], st.vz[i] = p[12];
-  }
-}
+constexpr float kMid = 8.0f;        // centre of V's codes
+constexpr uint32_t kLoMask = 0x000F000Fu, kHiMask = 0x00F000F0u;
 
 __device__ __forceinline__ half8_t frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   const u32x4_t w = {a, b, c, d};
   return __builtin_bit_cast(half8_t, w);
 }
 
+__device__ __forceinline__ f32x4_t mfma(half8_t a, half8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Two V codes less kMid, in units of 2^-24 (codes in bits 0-3) and 2^-20 (bits
+// 4-7): fp16 subnormals, every step exact.
+__device__ __forceinline__ uint32_t centred_lo(uint32_t w) {
+  constexpr uint32_t kOff = 0x80088008u;  // -8 * 2^-24, twice
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, w & kLoMask) + __builtin_bit_cast(half2_t, kOff));
+}
+__device__ __forceinline__ uint32_t centred_hi(uint32_t w) {
+  constexpr uint32_t kOff = 0x80808080u;  // -8 * 2^-20, twice
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, w & kHiMask) + __builtin_bit_cast(half2_t, kOff));
+}
+
 // fp16 value i of four packed dwords, as fp32
 __device__ __forceinline__ float half_of(const u32x4_t& w, int i) {
-  const half8_t h = __builtin_bit_cast(half8_t, w);
-  return static_cast<float>(h[i]);
-}
-
-__device__ __forceinline__ uint32_t restore2(uint32_t biased, half2_t bias, uint32_t s, uint32_t z) {
-  half2_t c = __builtin_bit_cast(half2_t, biased) - bias;  // exact
-  c = __builtin_elementwise_fma(c, __builtin_bit_cast(half2_t, s), __builtin_bit_cast(half2_t, z));
-  return __builtin_bit_cast(uint32_t, c);
-}
-
-template <int DT>
-__device__ __forceinline__ float half_bits(uint32_t h) {
-  return DT == kActF16 ? static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(h)))
-                       : __uint_as_float(h << 16);
+  return static_cast<float>(__builtin_bit_cast(half8_t, w)[i]);
 }
 
 struct SeqRange {
@@ -101,60 +98,99 @@ __device__ __forceinline__ SeqRange seq_range(const AttnArgs& a, int s) {
   return r;
 }
 
-// Rows of a sequence and key head: row r is token r / group, query head
-// r % group of the key head's group.
+// Operands made of a pair of dwords: K (low or high nibbles) and V.
+template <bool kHigh>
+__device__ __forceinline__ half8_t k_operand(uint32_t w0, uint32_t w1) {
+  constexpr uint32_t mask = kHigh ? kHiMask : kLoMask;
+  return frag(w0 & mask, (w0 >> 8) & mask, w1 & mask, (w1 >> 8) & mask);
+}
+template <bool kHigh>
+__device__ __forceinline__ half8_t v_operand(uint32_t w0, uint32_t w1) {
+  if (kHigh) return frag(centred_hi(w0), centred_hi(w0 >> 8), centred_hi(w1), centred_hi(w1 >> 8));
+  return frag(centred_lo(w0), centred_lo(w0 >> 8), centred_lo(w1), centred_lo(w1 >> 8));
+}
+
+// Codes of one block as a lane loads them.
+template <int D>
+struct KCodes {
+  u32x4_t w[D / 64];
+  // dword pair of half block t, scale group gr: values 64 gr .. 64 gr + 63
+  __device__ __forceinline__ u32x2_t pair(int t, int gr) const {
+    return D == 64 ? u32x2_t{w[0][2 * t], w[0][2 * t + 1]} : u32x2_t{w[t][2 * gr], w[t][2 * gr + 1]};
+  }
+};
+template <int D>
+struct VCodes {
+  u32x4_t w[D / 64];
+  // dword pair of values 32 i .. 32 i + 31
+  __device__ __forceinline__ u32x2_t pair(int i) const { return {w[i >> 1][2 * (i & 1)], w[i >> 1][2 * (i & 1) + 1]}; }
+};
+// Scales and zero points of the lane's eight tokens (fp16).
+template <int D>
+struct Params {
+  u32x4_t ks[D / 64], kz[D / 64], vs[D / 64], vz[D / 64];
+};
+
+template <int D>
+__device__ __forceinline__ void load_k(const uint8_t* blk, int lane, KCodes<D>& k) {
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i)
+    k.w[i] = *reinterpret_cast<const SHERRY_GLOBAL u32x4_t*>(gmem(blk) + i * 1024 + lane * 16);
+}
+template <int D>
+__device__ __forceinline__ void load_v(const uint8_t* blk, int lane, VCodes<D>& v) {
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i)
+    v.w[i] =
+        *reinterpret_cast<const SHERRY_GLOBAL u32x4_t*>(gmem(blk) + Kv4Layout<D>::kVOff + i * 1024 + lane * 16);
+}
+template <int D>
+__device__ __forceinline__ void load_p(const uint8_t* blk, int g, Params<D>& p) {
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const SHERRY_GLOBAL u32x4_t* s =
+        reinterpret_cast<const SHERRY_GLOBAL u32x4_t*>(gmem(blk) + Kv4Layout<D>::kPOff + i * 256 + g * 16);
+    p.ks[i] = s[0], p.kz[i] = s[4], p.vs[i] = s[8], p.vz[i] = s[12];
+  }
+}
+
+// Zeroes the scales of tokens that lie past `len` (their bytes may be anything,
+// and 0 * NaN is not 0); t0 is the lane's first token.
+template <int D>
+__device__ __forceinline__ Params<D> drop_tail(Params<D> p, int t0, int len) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + 16 * (i >> 1) + 2 * (i & 1);
+    const uint32_t mask = (t < len ? 0xFFFFu : 0u) | (t + 1 < len ? 0xFFFF0000u : 0u);
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) p.ks[k][i] &= mask, p.kz[k][i] &= mask, p.vs[k][i] &= mask, p.vz[k][i] &= mask;
+  }
+  return p;
+}
+
+// A lane's queries, values 32 i + 8 g .. + 7 of one row.
 template <int D, int DT>
-__global__ __launch_bounds__(kAttnThreads) void kv4_attn_kernel(AttnArgs a) {
-  constexpr int NG = D / 64;   // scale groups
-  constexpr int KS = D / 32;   // products along D per 16 tokens
-  constexpr int NT = D / 16;   // 16-value tiles of the output
-  constexpr int kPad = D + 4;  // LDS row stride: 16 rows start 4 banks apart
-  __shared__ float lds_o[kAttnWaves][16][kPad];
-  __shared__ float lds_m[kAttnWaves][16], lds_l[kAttnWaves][16];
-
-  const int split = static_cast<int>(blockIdx.x % a.splits);
-  const int st_id = static_cast<int>(blockIdx.x / a.splits);
-  const int seq = st_id / a.row_tiles;
-  const int tile = st_id - seq * a.row_tiles;
-  const int kvh = blockIdx.y;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int lane = threadIdx.x & (kWave - 1);
-  const int col = lane & 15, g = lane >> 4;
-  const SeqRange sr = seq_range(a, seq);
-  const int n = min(sr.n, a.max_q);
-  const int rows = n * a.group;
-  const int row0 = tile * 16;
-  if (row0 >= rows) return;
-  const int nrow = min(16, rows - row0);
-
-  // visible tokens: row r sees tokens below lim(r)
-  const int lim_lo = max(sr.len - sr.n + row0 / a.group + 1, 0);
-  const int lim_hi = max(min(sr.len - sr.n + (row0 + nrow - 1) / a.group + 1, sr.len), 0);
-  const int row = min(row0 + col, rows - 1);
-  const int tok = row / a.group;
-  const int head = kvh * a.group + (row - tok * a.group);
-  const int lim = sr.len - sr.n + tok + 1;
-
-  // the lane's queries: values 32 ks + 8 g .. + 7 of its row, scaled to fp16
-  half8_t q[KS];
-  float sumq[NG];
-  float kc;  // score scale
-  {
-    float f[KS][8];
-    float amax = 0.0f;
-    const int64_t at = (sr.first + tok) * a.q_st + head * a.q_sh + 8 * g;
+struct Queries {
+  float f[D / 32][8];
+  __device__ __forceinline__ void load(const void* q, int64_t at) {
 #pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      load8<DT>(a.q, at + 32 * i, f[i]);
+    for (int i = 0; i < D / 32; ++i) load8<DT>(q, at + 32 * i, f[i]);
+  }
+  // largest magnitude of the row, 0 if that is infinite (the row is spoiled, its
+  // neighbours are not)
+  __device__ __forceinline__ float top() const {
+    float m = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[i][j]));
-    }
-    amax = fmaxf(amax, __shfl_xor(amax, 16));
-    amax = fmaxf(amax, __shfl_xor(amax, 32));
-    const int e = max(static_cast<int>(__float_as_uint(amax) >> 23), 1) - 127;
-    const float unit = a.scale * kLog2e;
+    for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[i][j]));
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    return m < __builtin_inff() ? m : 0.0f;
+  }
+  __device__ __forceinline__ void sums(float unit, float (&sumq)[D / 64]) const {
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
       float s = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += f[2 * i][j] + f[2 * i + 1][j];
@@ -162,223 +198,695 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_attn_kernel(AttnArgs a) {
       s += __shfl_xor(s, 32);
       sumq[i] = s * unit;
     }
-#pragma unroll
-    for (int i = 0; i < KS; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        q[i][j] = static_cast<_Float16>(__builtin_ldexpf(f[i][j], 11 - e - 4 * (i & 1)));
-    kc = __builtin_ldexpf(unit, 24 + e - 11);
   }
+  // fp16 operands, the row's largest at 2^11, odd products (codes in bits 4-7)
+  // 2^-4 of that
+  __device__ __forceinline__ void operands(int e, half8_t (&q)[D / 32]) const {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[i][j] = static_cast<_Float16>(__builtin_ldexpf(f[i][j], 11 - e - 4 * (i & 1)));
+  }
+};
 
-  f32x4_t o[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) o[i] = f32x4_t{0, 0, 0, 0};
-  float m = kNoMax, l = 0.0f;
+__device__ __forceinline__ int exponent_of(float v) { return max(static_cast<int>(__float_as_uint(v) >> 23), 1) - 127; }
 
-  // this workgroup's blocks, taken by its waves in turn
-  const int nblk = (lim_hi + kKv4Block - 1) / kKv4Block;
-  const int per = (nblk + a.splits - 1) / a.splits;
-  const int b_end = min(nblk, (split + 1) * per);
-  const int page_blocks = a.c.page_shift - 5;
-  const int32_t* table = a.table + static_cast<int64_t>(seq) * a.table_stride;
-  for (int b = split * per + wave; b < b_end; b += kAttnWaves) {
-    const int64_t page = gmem(table)[b >> page_blocks];
-    if (page < 0 || page >= a.c.n_pages) continue;  // no such page: no such tokens
-    Stage<D> st;
-    load_block<D>(a.c.data + kv4_block_off<D>(a.c, page, kvh, b & ((1 << page_blocks) - 1)), lane, st);
-
-    f32x4_t acc[2][NG];
+// Running state of one tile of 16 rows: O^T (without the zero-point part), the
+// zero-point part, maximum and sum.
+template <int D>
+struct Acc {
+  f32x4_t o[D / 16];
+  float w[D / 64];
+  float m, l;
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < D / 16; ++i) o[i] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        const uint32_t w0 = D == 64 ? st.k[0][2 * t] : st.k[t][2 * i];
-        const uint32_t w1 = D == 64 ? st.k[0][2 * t + 1] : st.k[t][2 * i + 1];
-        const uint32_t h0 = w0 >> 8, h1 = w1 >> 8;
-        constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u;
-        f32x4_t c = {0, 0, 0, 0};
-        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(frag(w0 & kLo, h0 & kLo, w1 & kLo, h1 & kLo), q[2 * i], c, 0, 0, 0);
-        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(frag(w0 & kHi, h0 & kHi, w1 & kHi, h1 & kHi), q[2 * i + 1], c, 0, 0, 0);
-        acc[t][i] = c;
-      }
-
-    const int t0 = b * kKv4Block + 4 * g;  // the lane's tokens: t0 + i, t0 + 16 + i
-    const bool edge = (b + 1) * kKv4Block > lim_lo;
-    if (edge) {
-      // tokens past the sequence may hold anything: their V must be finite
+    for (int i = 0; i < D / 64; ++i) w[i] = 0.0f;
+    m = kNoMax, l = 0.0f;
+  }
+  __device__ __forceinline__ void scale(float f) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t keep = t0 + 16 * (i >> 2) + (i & 3) < sr.len ? 0xFFFFu << (16 * (i & 1)) : 0u;
-        const uint32_t mask = keep | ~(0xFFFFu << (16 * (i & 1)));
+    for (int i = 0; i < D / 16; ++i) o[i] *= f;
 #pragma unroll
-        for (int k = 0; k < NG; ++k) st.vs[k][i >> 1] &= mask, st.vz[k][i >> 1] &= mask;
-      }
+    for (int i = 0; i < D / 64; ++i) w[i] *= f;
+    l *= f;
+  }
+  // value i of tile nt: odd tiles are made of high nibbles
+  __device__ __forceinline__ float value(int nt, int i) const {
+    return __builtin_fmaf(o[nt][i], nt & 1 ? 1048576.0f : 16777216.0f, w[nt >> 2]);
+  }
+  // after the last block: sums over the four lane groups of a row
+  __device__ __forceinline__ void finish() {
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      w[i] += __shfl_xor(w[i], 16);
+      w[i] += __shfl_xor(w[i], 32);
     }
-    // x = score - m in powers of two
-    float x[8];
-    auto scores = [&](float mm) {
+  }
+};
+
+// The lane's eight tokens' parameters of group k: K scale (with the score scale
+// in it) and zero point, V scale, and V zero point + kMid V scale.
+template <int D>
+struct RawParams {  // made from fp16 as they are used
+  const Params<D>& p;
+  float kc;
+  __device__ __forceinline__ float ks(int k, int i) const { return __builtin_fmaf(half_of(p.ks[k], i), kc, 0.0f); }
+  __device__ __forceinline__ float kz(int k, int i) const { return half_of(p.kz[k], i); }
+  __device__ __forceinline__ float vs(int k, int i) const { return half_of(p.vs[k], i); }
+  __device__ __forceinline__ float zc(int k, int i) const {
+    return __builtin_fmaf(half_of(p.vs[k], i), kMid, half_of(p.vz[k], i));
+  }
+};
+template <int D>
+struct LdsParams {  // ready-made, in LDS (at the lane group's eight tokens)
+  const float* at;
+  __device__ __forceinline__ float ks(int k, int i) const { return at[(4 * k) * kKv4Block + i]; }
+  __device__ __forceinline__ float kz(int k, int i) const { return at[(4 * k + 1) * kKv4Block + i]; }
+  __device__ __forceinline__ float vs(int k, int i) const { return at[(4 * k + 2) * kKv4Block + i]; }
+  __device__ __forceinline__ float zc(int k, int i) const { return at[(4 * k + 3) * kKv4Block + i]; }
+};
+
+// The softmax step of one tile: scores from the products c (S^T of each scale
+// group) to P operands, one per group.  kEdge: tokens from lim on are not seen
+// (t0 is the lane's first token).
+template <int D, bool kEdge, class P>
+__device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D / 64], const P& pr,
+                                             const float (&sumq)[D / 64], int t0, int lim, half8_t (&pf)[D / 64]) {
+  constexpr int NG = D / 64;
+  float p[8], ps[NG][8], top, sum;
+  auto score = [&](int i, float m) {
+    float u = __builtin_fmaf(pr.kz(0, i), sumq[0], -m);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float s = half_of(st.ks[0], i) * acc[i >> 2][0][i & 3];
-        float u = __builtin_fmaf(half_of(st.kz[0], i), sumq[0], -mm);
-        if constexpr (NG == 2) {
-          s = __builtin_fmaf(half_of(st.ks[1], i), acc[i >> 2][1][i & 3], s);
-          u = __builtin_fmaf(half_of(st.kz[1], i), sumq[1], u);
-        }
-        x[i] = __builtin_fmaf(s, kc, u);
-      }
-      if (edge) {
+    for (int k = 1; k < NG; ++k) u = __builtin_fmaf(pr.kz(k, i), sumq[k], u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = t0 + 16 * (i >> 2) + (i & 3) < lim ? x[i] : -__builtin_inff();
-      }
-    };
-    auto top = [&]() {
-      return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    };
-    scores(m - kPExp);
-    if (__any(top() > kPExp + kSlack)) {
-      scores(0.0f);
-      float mx = top();
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      const float m_new = fmaxf(m, mx);
-      const float alpha = __builtin_amdgcn_exp2f(m - m_new);
-      m = m_new;
-      l *= alpha;
-#pragma unroll
-      for (int i = 0; i < NT; ++i) o[i] *= alpha;
-      scores(m - kPExp);
-    }
-    float p[8];
+    for (int k = 0; k < NG; ++k) u = __builtin_fmaf(pr.ks(k, i), c[i >> 2][k][i & 3], u);
+    if constexpr (kEdge) u = t0 + 16 * (i >> 2) + (i & 3) < lim ? u : -__builtin_inff();
+    return u;
+  };
+  auto weights = [&]() {
+    top = 0.0f, sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(x[i]);
-      l += p[i];
+      p[i] = __builtin_amdgcn_exp2f(score(i, a.m - kPExp));
+      sum += p[i];
     }
-    const half8_t pf = frag(pack2<kActF16>(p[0], p[1]), pack2<kActF16>(p[2], p[3]), pack2<kActF16>(p[4], p[5]),
-                            pack2<kActF16>(p[6], p[7]));
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      constexpr half2_t k1024 = {static_cast<_Float16>(1024.0f), static_cast<_Float16>(1024.0f)};
-      constexpr half2_t k64 = {static_cast<_Float16>(64.0f), static_cast<_Float16>(64.0f)};
-      const u32x4_t vs = st.vs[i >> 1], vz = st.vz[i >> 1];
-      uint32_t lo[4], hi[4];
+    for (int k = 0; k < NG; ++k)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint32_t w = st.v[i >> 1][2 * (i & 1) + t], h = w >> 8;
-        lo[2 * t] = restore2((w & 0x000F000Fu) | 0x64006400u, k1024, vs[2 * t], vz[2 * t]);
-        lo[2 * t + 1] = restore2((h & 0x000F000Fu) | 0x64006400u, k1024, vs[2 * t + 1], vz[2 * t + 1]);
-        hi[2 * t] = restore2((w & 0x00F000F0u) | 0x54005400u, k64, vs[2 * t], vz[2 * t]);
-        hi[2 * t + 1] = restore2((h & 0x00F000F0u) | 0x54005400u, k64, vs[2 * t + 1], vz[2 * t + 1]);
+      for (int i = 0; i < 8; ++i) {
+        ps[k][i] = __builtin_fmaf(p[i], pr.vs(k, i), 0.0f);  // (fma: a mixed-precision instruction for fp16)
+        top = fmaxf(top, ps[k][i]);
       }
-      o[2 * i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(frag(lo[0], lo[1], lo[2], lo[3]), pf, o[2 * i], 0, 0, 0);
-      o[2 * i + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(frag(hi[0], hi[1], hi[2], hi[3]), pf, o[2 * i + 1], 0, 0, 0);
+  };
+  weights();
+  if (__builtin_expect(__any(top > kPTop || sum > kSumTop), 0)) {
+    float mx = kNoMax;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v = 5.9604644775390625e-8f;  // 2^-24
+#pragma unroll
+      for (int k = 0; k < NG; ++k) v = fmaxf(v, pr.vs(k, i));
+      mx = fmaxf(mx, score(i, 0.0f) + __builtin_amdgcn_logf(v));  // log2
     }
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float m_new = fmaxf(a.m, mx);
+    a.scale(__builtin_amdgcn_exp2f(a.m - m_new));
+    a.m = m_new;
+    weights();
+  }
+  a.l += sum;
+#pragma unroll
+  for (int k = 0; k < NG; ++k) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a.w[k] = __builtin_fmaf(p[i], pr.zc(k, i), a.w[k]);
+    pf[k] = frag(pack2<kActF16>(ps[k][0], ps[k][1]), pack2<kActF16>(ps[k][2], ps[k][3]),
+                 pack2<kActF16>(ps[k][4], ps[k][5]), pack2<kActF16>(ps[k][6], ps[k][7]));
+  }
+}
+
+// Stores of a row's result, four values d .. d + 3: the final one, or a split's
+// share.
+template <int D, int DT>
+__device__ __forceinline__ void store_row(const AttnArgs& a, int split, int64_t token, int head, int d,
+                                          const float (&v)[4], float m, float l) {
+  if (a.splits > 1) {
+    const int64_t at = (static_cast<int64_t>(split) * a.n_tokens + token) * a.n_q_heads + head;
+    *gmem(reinterpret_cast<f32x4_t*>(a.part_o + at * D + d)) = f32x4_t{v[0], v[1], v[2], v[3]};
+    if (d == 0) *gmem(reinterpret_cast<f32x2_t*>(a.part_ml + at * 2)) = f32x2_t{m, l};
+  } else {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const u32x2_t out = {pack2<DT>(v[0] * inv, v[1] * inv), pack2<DT>(v[2] * inv, v[3] * inv)};
+    *gmem(reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + token * a.o_st + head * a.o_sh + d)) = out;
+    if (a.lse && d == 0)
+      gmem(a.lse)[token * a.n_q_heads + head] =
+          l == 0.0f ? -__builtin_inff() : (m - kPExp + __builtin_log2f(l)) * kLn2;
+  }
+}
+
+// ---- up to 16 rows: the cached tokens are what there is to share out ----
+//
+// The workgroup's waves take chunks of G blocks in turn.  With at most 16 / G
+// rows, the 16 columns of a tile hold the rows G times over, and the columns of
+// copy b are given to block b of the chunk: the products of the G blocks add
+// into one S^T, each with the queries zeroed outside its columns, so one
+// softmax step serves G blocks.  The copies are separate softmaxes, joined with
+// the waves' at the end.  (Rows <= 8: G = 2 against G = 1, same box: 22.4
+// against 23.4 us for one token over 131072, 90 against 104 us for a batch of
+// 48; G = 4 for rows <= 4 costs more registers than it saves: 26 and 107 us.)
+//
+// K of the next chunk is loaded as soon as this one's has been multiplied, V
+// and the scales likewise, so loads are in flight during the softmax and the
+// other product; the page numbers are read a chunk ahead of that.  After the
+// last chunk the loads repeat it (from L2): a branch around them would make the
+// compiler wait for them where it joins.
+template <int D, int DT, int G>
+__global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs a) {
+  constexpr int NG = D / 64, KS = D / 32, NT = D / 16;
+  constexpr int kRows = 16 / G;
+  constexpr int kPad = D + 4;  // LDS row stride: 16 rows start 4 banks apart
+  __shared__ float lds_o[kAttnWaves][16][kPad];
+  __shared__ float lds_m[kAttnWaves][16], lds_l[kAttnWaves][16];
+
+  const int split = static_cast<int>(blockIdx.x % a.splits);
+  const int st_id = static_cast<int>(blockIdx.x / a.splits);
+  const int seq = st_id / a.row_tiles;
+  const int row0 = (st_id - seq * a.row_tiles) * kRows;
+  const int kvh = blockIdx.y;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & (kWave - 1);
+  const int col = lane & 15, g = lane >> 4;
+  const int copy = col / kRows;
+  const SeqRange sr = seq_range(a, seq);
+  const int rows = min(sr.n, a.max_q) * a.group;
+  if (row0 >= rows) return;
+  const int nrow = min(kRows, rows - row0);
+
+  // row r sees tokens below lim(r)
+  const int lim_lo = max(sr.len - sr.n + row0 / a.group + 1, 0);
+  const int lim_hi = max(min(sr.len - sr.n + (row0 + nrow - 1) / a.group + 1, sr.len), 0);
+  const int row = min(row0 + col % kRows, rows - 1);
+  const int tok = row / a.group;
+  const int head = kvh * a.group + (row - tok * a.group);
+  const int lim = sr.len - sr.n + tok + 1;
+
+  const int nblk = (lim_hi + kKv4Block - 1) / kKv4Block;
+  const int chunks = (nblk + G - 1) / G;
+  const int per = (chunks + a.splits - 1) / a.splits;
+  const int c_end = min(chunks, (split + 1) * per);
+  const int c_begin = split * per + wave;
+  const int page_blocks = a.c.page_shift - 5;
+  const SHERRY_GLOBAL int32_t* table = gmem(a.table) + static_cast<int64_t>(seq) * a.table_stride;
+
+  struct Chunk {
+    const uint8_t* at[G];  // its blocks; one that is not there reads the cache's first
+    const uint8_t* mine;   // the block of the lane's copy
+    bool mine_there, all_there;
+  };
+  auto pages = [&](int ch, int32_t (&pg)[G]) {
+#pragma unroll
+    for (int b = 0; b < G; ++b) pg[b] = table[min(ch * G + b, nblk - 1) >> page_blocks];
+  };
+  auto chunk = [&](int ch, const int32_t (&pg)[G]) {
+    Chunk c;
+    c.all_there = true;
+#pragma unroll
+    for (int b = 0; b < G; ++b) {
+      const int blk = ch * G + b;
+      const bool there = blk < nblk && pg[b] >= 0 && pg[b] < a.c.n_pages;
+      const int64_t off = kv4_block_off<D>(a.c, there ? pg[b] : 0, kvh, blk & ((1 << page_blocks) - 1));
+      const uint8_t* at = a.c.data + (there ? off : 0);
+      c.at[b] = at;
+      c.mine = b == 0 || copy == b ? at : c.mine;
+      c.mine_there = b == 0 || copy == b ? there : c.mine_there;
+      c.all_there = c.all_there && there;
+    }
+    return c;
+  };
+  KCodes<D> k[G];
+  VCodes<D> v[G];
+  Params<D> pr;
+  Chunk now, next;
+  int32_t pg[G];
+  const bool any = c_begin < c_end;
+  if (any) {
+    pages(c_begin, pg);
+    now = chunk(c_begin, pg);
+#pragma unroll
+    for (int b = 0; b < G; ++b) load_k<D>(now.at[b], lane, k[b]);
+    load_p<D>(now.mine, g, pr);
+#pragma unroll
+    for (int b = 0; b < G; ++b) load_v<D>(now.at[b], lane, v[b]);
+    pages(min(c_begin + kAttnWaves, c_end - 1), pg);
   }
 
-  // join the waves: every wave's rows on a common maximum
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
-  if (col < nrow) {
-    if (g == 0) lds_m[wave][col] = m, lds_l[wave][col] = l;
+  half8_t q[G][KS];
+  float sumq[NG];
+  float kc;
+  {
+    Queries<D, DT> f;
+    f.load(a.q, (sr.first + tok) * a.q_st + head * a.q_sh + 8 * g);
+    const int e = exponent_of(f.top());
+    const float unit = a.scale * kLog2e;
+    f.sums(unit, sumq);
+    kc = __builtin_ldexpf(unit, 24 + e - 11);
+    half8_t t[KS];
+    f.operands(e, t);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4_t*>(&lds_o[wave][col][16 * i + 4 * g]) = o[i];
+    for (int b = 0; b < G; ++b)
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        u32x4_t w = __builtin_bit_cast(u32x4_t, t[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = copy == b ? w[j] : 0u;
+        q[b][i] = __builtin_bit_cast(half8_t, w);
+      }
+  }
+
+  Acc<D> acc;
+  acc.clear();
+  if (any) {
+    next = chunk(min(c_begin + kAttnWaves, c_end - 1), pg);
+    auto step = [&](int ch, auto edge) {
+      pages(min(ch + 2 * kAttnWaves, c_end - 1), pg);
+      f32x4_t c[2][NG];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < NG; ++i) c[t][i] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int b = 0; b < G; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+              const u32x2_t w = k[b].pair(t, i);
+              c[t][i] = mfma(e ? k_operand<true>(w.x, w.y) : k_operand<false>(w.x, w.y), q[b][2 * i + e], c[t][i]);
+            }
+#pragma unroll
+      for (int b = 0; b < G; ++b) load_k<D>(next.at[b], lane, k[b]);
+      const int t0 = (ch * G + copy) * kKv4Block + 4 * g;
+      half8_t pf[NG];
+      if constexpr (edge.value)
+      {
+        const Params<D> seen = drop_tail<D>(pr, t0, now.mine_there ? sr.len : 0);
+        softmax_step<D, true>(acc, c, RawParams<D>{seen, kc}, sumq, t0, now.mine_there ? lim : 0, pf);
+      } else {
+        softmax_step<D, false>(acc, c, RawParams<D>{pr, kc}, sumq, t0, lim, pf);
+      }
+      load_p<D>(next.mine, g, pr);
+#pragma unroll
+      for (int b = 0; b < G; ++b)
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+          u32x4_t pw = __builtin_bit_cast(u32x4_t, pf[i]);
+          if constexpr (G > 1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pw[j] = copy == b ? pw[j] : 0u;
+          }
+          const half8_t pb = __builtin_bit_cast(half8_t, pw);
+#pragma unroll
+          for (int j = 2 * i; j < 2 * i + 2; ++j) {
+            const u32x2_t w = v[b].pair(j);
+            acc.o[2 * j] = mfma(v_operand<false>(w.x, w.y), pb, acc.o[2 * j]);
+            acc.o[2 * j + 1] = mfma(v_operand<true>(w.x, w.y), pb, acc.o[2 * j + 1]);
+          }
+        }
+#pragma unroll
+      for (int b = 0; b < G; ++b) load_v<D>(next.at[b], lane, v[b]);
+      now = next;
+      next = chunk(min(ch + 2 * kAttnWaves, c_end - 1), pg);
+    };
+    const int whole = lim_lo / (G * kKv4Block);  // chunks that every row sees all of
+    int ch = c_begin;
+    for (; ch < min(whole, c_end) && now.all_there; ch += kAttnWaves) step(ch, std::false_type{});
+    for (; ch < c_end; ch += kAttnWaves) step(ch, std::true_type{});
+  }
+
+  // join the waves and copies: every row's shares on a common maximum
+  acc.finish();
+  if (col % kRows < nrow) {
+    if (g == 0) lds_m[wave][col] = acc.m, lds_l[wave][col] = acc.l;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      f32x4_t t;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t[j] = acc.value(i, j);
+      *reinterpret_cast<f32x4_t*>(&lds_o[wave][col][16 * i + 4 * g]) = t;
+    }
   }
   __syncthreads();
   for (int u = threadIdx.x; u < nrow * (D / 4); u += kAttnThreads) {
     const int r = u / (D / 4), d = 4 * (u % (D / 4));
-    float mm = lds_m[0][r];
+    float m = kNoMax, l = 0.0f, o[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int w = 1; w < kAttnWaves; ++w) mm = fmaxf(mm, lds_m[w][r]);
-    float ll = 0.0f;
-    f32x4_t v = {0, 0, 0, 0};
+    for (int w = 0; w < kAttnWaves * G; ++w) m = fmaxf(m, lds_m[w / G][r + kRows * (w % G)]);
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) {
-      const float f = __builtin_amdgcn_exp2f(lds_m[w][r] - mm);
-      ll = __builtin_fmaf(f, lds_l[w][r], ll);
-      const f32x4_t t = *reinterpret_cast<const f32x4_t*>(&lds_o[w][r][d]);
+    for (int w = 0; w < kAttnWaves * G; ++w) {
+      const int cc = r + kRows * (w % G);
+      const float f = __builtin_amdgcn_exp2f(lds_m[w / G][cc] - m);
+      l = __builtin_fmaf(f, lds_l[w / G][cc], l);
+      const f32x4_t t = *reinterpret_cast<const f32x4_t*>(&lds_o[w / G][cc][d]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(f, t[j], v[j]);
+      for (int j = 0; j < 4; ++j) o[j] = __builtin_fmaf(f, t[j], o[j]);
     }
-    const int rr = row0 + r;
-    const int ti = rr / a.group;
-    const int64_t token = sr.first + ti;
-    const int hd = kvh * a.group + (rr - ti * a.group);
-    if (a.splits > 1) {
-      const int64_t at = (static_cast<int64_t>(split) * a.n_tokens + token) * a.n_q_heads + hd;
-      *gmem(reinterpret_cast<f32x4_t*>(a.part_o + at * D + d)) = v;
-      if (d == 0) *gmem(reinterpret_cast<f32x2_t*>(a.part_ml + at * 2)) = f32x2_t{mm, ll};
-    } else {
-      const float inv = ll > 0.0f ? 1.0f / ll : (ll == 0.0f ? 0.0f : ll);
-      u32x2_t out = {pack2<DT>(v[0] * inv, v[1] * inv), pack2<DT>(v[2] * inv, v[3] * inv)};
-      *gmem(reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + token * a.o_st + hd * a.o_sh + d)) = out;
-      if (a.lse && d == 0)
-        gmem(a.lse)[token * a.n_q_heads + hd] =
-            ll == 0.0f ? -__builtin_inff() : (mm - kPExp + __builtin_log2f(ll)) * kLn2;
+    const int rr = row0 + r, ti = rr / a.group;
+    store_row<D, DT>(a, split, sr.first + ti, kvh * a.group + (rr - ti * a.group), d, o, m, l);
+  }
+}
+
+// ---- more rows: a wave takes R tiles of 16 rows of its own ----
+//
+// Here the products and the softmax are the work, so a block is unpacked once
+// for the workgroup's 64 R rows: each wave makes a quarter of the K and V
+// operands and of the parameters (fp32, the score scale in K's), in LDS in the
+// order of the product's lanes (16-byte accesses without conflicts).  Two
+// buffers: while block b is used, block b + 1 is unpacked behind it and the
+// codes of b + 2 are loaded; one barrier a block.
+template <int D>
+struct RowsBuf {
+  u32x4_t k[2 * D / 32][kWave], v[D / 16][kWave];
+  float par[4 * (D / 64)][kKv4Block];  // [group, kind][lane group's eight tokens in turn]
+};
+
+template <int D, int DT, int R>
+__global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs a) {
+  using L = Kv4Layout<D>;
+  constexpr int NG = D / 64, KS = D / 32, NT = D / 16;
+  constexpr int kRows = 16 * R * kAttnWaves;
+  __shared__ RowsBuf<D> lds[2];
+  __shared__ float lds_top[kAttnWaves];
+  // the queries of two tiles at D = 128 would not fit the registers of two waves
+  constexpr bool kLdsQ = D == 128 && R > 1;
+  __shared__ u32x4_t lds_q[kLdsQ ? kAttnWaves : 1][kLdsQ ? R : 1][kLdsQ ? KS : 1][kWave];
+  const int split = static_cast<int>(blockIdx.x % a.splits);
+  const int st_id = static_cast<int>(blockIdx.x / a.splits);
+  const int seq = st_id / a.row_tiles;
+  const int kvh = blockIdx.y;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & (kWave - 1);
+  const int col = lane & 15, g = lane >> 4;
+  const SeqRange sr = seq_range(a, seq);
+  const int rows = min(sr.n, a.max_q) * a.group;
+  // the last rows see most tokens: they start first
+  const int wg0 = (a.row_tiles - 1 - (st_id - seq * a.row_tiles)) * kRows;
+  if (wg0 >= rows) return;
+  const int row0 = wg0 + wave * 16 * R;
+  const bool has_rows = row0 < rows;  // a wave without rows still unpacks
+  auto limit = [&](int row) { return max(min(sr.len - sr.n + row / a.group + 1, sr.len), 0); };
+  const int lim_lo = limit(wg0), lim_hi = limit(min(wg0 + kRows, rows) - 1);
+  const int wave_hi = limit(min(row0 + 16 * R, rows) - 1);
+
+  const int nblk = (lim_hi + kKv4Block - 1) / kKv4Block;
+  const int per = (nblk + a.splits - 1) / a.splits;
+  const int b_begin = split * per, b_end = min(nblk, b_begin + per);
+  const int page_blocks = a.c.page_shift - 5;
+  const SHERRY_GLOBAL int32_t* table = gmem(a.table) + static_cast<int64_t>(seq) * a.table_stride;
+  auto block = [&](int b, bool& there) {  // one that is not there reads the cache's first
+    const int32_t pg = table[b >> page_blocks];
+    there = pg >= 0 && pg < a.c.n_pages;
+    const int64_t off = kv4_block_off<D>(a.c, there ? pg : 0, kvh, b & ((1 << page_blocks) - 1));
+    return gmem(static_cast<const uint8_t*>(a.c.data)) + (there ? off : 0);
+  };
+  // the wave's share of a block: a pair of dwords a lane of K and of V (at
+  // D = 64 of one of them), and of the parameters one value a thread
+  constexpr bool kBoth = D == 128;
+  const int share = kBoth ? wave : wave & 1;
+  const bool does_k = kBoth || wave < 2, does_v = kBoth || wave >= 2;
+  const int k_at = D == 64 ? lane * 16 + share * 8 : (share >> 1) * 1024 + lane * 16 + (share & 1) * 8;
+  const int v_at = L::kVOff + (share >> 1) * 1024 + lane * 16 + (share & 1) * 8;
+  const int kind = (threadIdx.x >> 5) & 3, idx = threadIdx.x & 31;
+  const bool does_p = threadIdx.x < NG * 128;
+  const int p_at = L::kPOff + (threadIdx.x >> 7) * 256 + idx * 2;
+  u32x2_t kw = {0, 0}, vw = {0, 0};
+  uint16_t p0 = 0, p1 = 0;
+  auto fetch = [&](const SHERRY_GLOBAL uint8_t* blk) {
+    if (does_k) kw = *reinterpret_cast<const SHERRY_GLOBAL u32x2_t*>(blk + k_at);
+    if (does_v) vw = *reinterpret_cast<const SHERRY_GLOBAL u32x2_t*>(blk + v_at);
+    if (does_p) {
+      p0 = *reinterpret_cast<const SHERRY_GLOBAL uint16_t*>(blk + p_at + kind * 64);
+      p1 = *reinterpret_cast<const SHERRY_GLOBAL uint16_t*>(blk + p_at + 128);  // V's scale
+    }
+  };
+  float kc = 0.0f;
+  auto unpack = [&](int b, RowsBuf<D>& to) {
+    if (does_k) {
+      // products of K: half block t, group gr -> operands 2 gr (low nibbles) and 2 gr + 1
+      const int t = D == 64 ? share : share >> 1, gr = D == 64 ? 0 : share & 1;
+      to.k[t * KS + 2 * gr][lane] = __builtin_bit_cast(u32x4_t, k_operand<false>(kw.x, kw.y));
+      to.k[t * KS + 2 * gr + 1][lane] = __builtin_bit_cast(u32x4_t, k_operand<true>(kw.x, kw.y));
+    }
+    if (does_v) {
+      to.v[2 * share][lane] = __builtin_bit_cast(u32x4_t, v_operand<false>(vw.x, vw.y));
+      to.v[2 * share + 1][lane] = __builtin_bit_cast(u32x4_t, v_operand<true>(vw.x, vw.y));
+    }
+    if (does_p) {
+      // tokens past the sequence may hold anything: their parameters are 0
+      const int tok = b * kKv4Block + 16 * ((idx >> 2) & 1) + 4 * (idx >> 3) + (idx & 3);
+      const float x = static_cast<float>(__builtin_bit_cast(_Float16, p0));
+      const float s = static_cast<float>(__builtin_bit_cast(_Float16, p1));
+      const float v = kind == 0 ? x * kc : (kind == 3 ? __builtin_fmaf(s, kMid, x) : x);
+      to.par[(threadIdx.x >> 7) * 4 + kind][idx] = tok < sr.len ? v : 0.0f;
+    }
+  };
+  bool now_there = false, next_there = false;
+  if (b_begin < b_end) fetch(block(b_begin, now_there));
+
+  half8_t q[R][KS];
+  float sumq[R][NG];
+  int lim[R];
+  {
+    Queries<D, DT> f[R];
+    float top = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = min(row0 + 16 * r + col, rows - 1);
+      const int tok = row / a.group, head = kvh * a.group + (row - tok * a.group);
+      lim[r] = sr.len - sr.n + tok + 1;
+      f[r].load(a.q, (sr.first + tok) * a.q_st + head * a.q_sh + 8 * g);
+      top = fmaxf(top, f[r].top());
+    }
+    // one exponent for the workgroup's rows (the score scale is in the shared
+    // parameters): a row 2^-25 times smaller than the largest has scores that
+    // much smaller too
+    top = fmaxf(top, __shfl_xor(top, 1));
+    top = fmaxf(top, __shfl_xor(top, 2));
+    top = fmaxf(top, __shfl_xor(top, 4));
+    top = fmaxf(top, __shfl_xor(top, 8));
+    if (lane == 0) lds_top[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, lds_top[w]);
+    const int e = exponent_of(top);
+    const float unit = a.scale * kLog2e;
+    kc = __builtin_ldexpf(unit, 24 + e - 11);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      f[r].sums(unit, sumq[r]);
+      f[r].operands(e, q[r]);
+      if constexpr (kLdsQ) {  // (read by the wave that writes them)
+#pragma unroll
+        for (int i = 0; i < KS; ++i) lds_q[wave][r][i][lane] = __builtin_bit_cast(u32x4_t, q[r][i]);
+      }
+    }
+  }
+  Acc<D> acc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r].clear();
+  if (b_begin < b_end) {
+    unpack(b_begin, lds[0]);
+    fetch(block(min(b_begin + 1, b_end - 1), next_there));
+    __syncthreads();
+  }
+
+  auto step = [&](int b, auto edge) {
+    const RowsBuf<D>& from = lds[(b - b_begin) & 1];
+    if (now_there && has_rows && (!edge.value || b * kKv4Block < wave_hi)) {
+      f32x4_t c[R][2][NG];
+#pragma unroll
+      for (int i = 0; i < NG; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          half8_t qi[R];
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            qi[r] = kLdsQ ? __builtin_bit_cast(half8_t, lds_q[wave][r][2 * i + e][lane]) : q[r][2 * i + e];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const half8_t k = __builtin_bit_cast(half8_t, from.k[t * KS + 2 * i + e][lane]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) c[r][t][i] = mfma(k, qi[r], e ? c[r][t][i] : f32x4_t{0, 0, 0, 0});
+          }
+        }
+      const int t0 = b * kKv4Block + 4 * g;
+      half8_t pf[R][NG];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        softmax_step<D, edge.value>(acc[r], c[r], LdsParams<D>{&from.par[0][8 * g]}, sumq[r], t0, lim[r], pf[r]);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const half8_t v = __builtin_bit_cast(half8_t, from.v[i][lane]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r].o[i] = mfma(v, pf[r][i >> 2], acc[r].o[i]);
+      }
+    }
+    now_there = next_there;
+    if (b + 1 < b_end) {
+      unpack(b + 1, lds[(b + 1 - b_begin) & 1]);
+      fetch(block(min(b + 2, b_end - 1), next_there));
+      __syncthreads();
+    }
+  };
+  const int whole = lim_lo / kKv4Block;  // blocks that every row sees all of
+  int b = b_begin;
+  for (; b < min(whole, b_end); ++b) step(b, std::false_type{});
+  for (; b < b_end; ++b) step(b, std::true_type{});
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    acc[r].finish();
+    const int row = row0 + 16 * r + col;
+    if (row >= rows) continue;
+    const int tok = row / a.group, head = kvh * a.group + (row - tok * a.group);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      float o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = acc[r].value(i, j);
+      store_row<D, DT>(a, split, sr.first + tok, head, 16 * i + 4 * g, o, acc[r].m, acc[r].l);
     }
   }
 }
 
-// Joins the splits of every row: a quarter of a wave (D = 64) or half of one
-// (D = 128) per row, four values a lane, splits in their order.
+// Joins the splits of every row.  A row takes D / 4 lanes (four values each)
+// times 1 << sg_shift groups, and group i the splits i, i + groups, ...: first
+// the largest maximum, then the sums, so that no load waits for another.
 template <int D, int DT>
-__global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(AttnArgs a, int join_blocks, int sg_shift) {
   constexpr int kLanes = D / 4;
-  const int seq = static_cast<int>(blockIdx.x / a.join_blocks);
+  __shared__ f32x4_t lds_o[kAttnThreads];
+  __shared__ f32x2_t lds_ml[kAttnThreads];
+  const int seq = static_cast<int>(blockIdx.x / join_blocks);
   const SeqRange sr = seq_range(a, seq);
-  const int n = min(sr.n, a.max_q);
+  const int groups = 1 << sg_shift;
+  const int lane = threadIdx.x % kLanes;
+  const int grp = (threadIdx.x / kLanes) & (groups - 1);
   const int64_t u =
-      (static_cast<int64_t>(blockIdx.x % a.join_blocks) * kAttnThreads + threadIdx.x) / kLanes;
-  const int d = 4 * (threadIdx.x % kLanes);
+      (static_cast<int64_t>(blockIdx.x % join_blocks) * (kAttnThreads / kLanes) >> sg_shift) +
+      (threadIdx.x / kLanes >> sg_shift);
   const int64_t ti = u / a.n_q_heads;
-  if (ti >= n) return;
+  const bool live = ti < min(sr.n, a.max_q);
   const int hd = static_cast<int>(u - ti * a.n_q_heads);
   const int64_t token = sr.first + ti;
   const int64_t at = token * a.n_q_heads + hd, step = a.n_tokens * a.n_q_heads;
   float m = kNoMax, l = 0.0f;
   f32x4_t v = {0, 0, 0, 0};
-  for (int s = 0; s < a.splits; ++s) {
-    const f32x2_t ml = *gmem(reinterpret_cast<const f32x2_t*>(a.part_ml + (at + s * step) * 2));
-    const f32x4_t t = *gmem(reinterpret_cast<const f32x4_t*>(a.part_o + (at + s * step) * D + d));
-    const float m_new = fmaxf(m, ml.x);
-    const float f0 = __builtin_amdgcn_exp2f(m - m_new), f1 = __builtin_amdgcn_exp2f(ml.x - m_new);
-    m = m_new;
-    l = __builtin_fmaf(f1, ml.y, l * f0);
+  if (live) {
+    const SHERRY_GLOBAL f32x2_t* ml = gmem(reinterpret_cast<const f32x2_t*>(a.part_ml)) + at;
+    const SHERRY_GLOBAL f32x4_t* po = gmem(reinterpret_cast<const f32x4_t*>(a.part_o)) + at * kLanes + lane;
+#pragma unroll 4
+    for (int s = grp; s < a.splits; s += groups) m = fmaxf(m, ml[s * step].x);
+#pragma unroll 4
+    for (int s = grp; s < a.splits; s += groups) {
+      const f32x2_t t = ml[s * step];
+      const f32x4_t o = po[s * step * kLanes];
+      const float f = __builtin_amdgcn_exp2f(t.x - m);
+      l = __builtin_fmaf(f, t.y, l);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(f1, t[j], v[j] * f0);
+      for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(f, o[j], v[j]);
+    }
   }
-  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-  u32x2_t out = {pack2<DT>(v[0] * inv, v[1] * inv), pack2<DT>(v[2] * inv, v[3] * inv)};
-  *gmem(reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + token * a.o_st + hd * a.o_sh + d)) = out;
-  if (a.lse && d == 0)
-    gmem(a.lse)[at] = l == 0.0f ? -__builtin_inff() : (m - kPExp + __builtin_log2f(l)) * kLn2;
+  if (groups > 1) {
+    lds_o[threadIdx.x] = v;
+    lds_ml[threadIdx.x] = f32x2_t{m, l};
+    __syncthreads();
+    if (grp != 0) return;
+    for (int i = 1; i < groups; ++i) m = fmaxf(m, lds_ml[threadIdx.x + i * kLanes].x);
+    l = 0.0f;
+    v = f32x4_t{0, 0, 0, 0};
+    for (int i = 0; i < groups; ++i) {
+      const f32x2_t t = lds_ml[threadIdx.x + i * kLanes];
+      const f32x4_t o = lds_o[threadIdx.x + i * kLanes];
+      const float f = __builtin_amdgcn_exp2f(t.x - m);
+      l = __builtin_fmaf(f, t.y, l);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(f, o[j], v[j]);
+    }
+  }
+  if (!live) return;
+  AttnArgs one = a;
+  one.splits = 1;  // the final store
+  const float o[4] = {v[0], v[1], v[2], v[3]};
+  store_row<D, DT>(one, 0, token, hd, 4 * lane, o, m, l);
+}
+
+// How a call is cut up: rows per workgroup (in tiles of 16, `r` a wave, or fewer
+// than 16 in one), and the splits of the cached tokens.
+struct AttnShape {
+  int g;  // blocks per softmax step (rows <= 16 / g), 0: rows kernel
+  int r;  // 16-row tiles per wave of the rows kernel
+};
+
+AttnShape attn_shape(int64_t rows, int head_dim) {
+  if (rows <= 8) return {2, 0};
+  if (rows <= 16) return {1, 0};
+  if (rows <= 16 * kAttnWaves) return {0, 1};
+  if (rows <= 32 * kAttnWaves || head_dim == 128) return {0, 2};
+  return {0, 4};
 }
 
 template <int D, int DT>
 hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.splits) * a.n_seqs * a.row_tiles),
                   static_cast<unsigned>(a.c.n_kv_heads));
-  hipLaunchKernelGGL((kv4_attn_kernel<D, DT>), grid, dim3(kAttnThreads), 0, stream, a);
+  const AttnShape s = attn_shape(static_cast<int64_t>(a.max_q) * a.group, D);
+  const dim3 block(kAttnThreads);
+  if (s.g == 2) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 2>), grid, block, 0, stream, a);
+  else if (s.g == 1) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 1>), grid, block, 0, stream, a);
+  else if (s.r == 1) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 1>), grid, block, 0, stream, a);
+  else if (s.r == 2) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 2>), grid, block, 0, stream, a);
+  else if constexpr (D == 64) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 4>), grid, block, 0, stream, a);
   if (a.splits > 1) {
-    AttnArgs j = a;
-    j.join_blocks = static_cast<int32_t>(
-        (static_cast<int64_t>(a.max_q) * a.n_q_heads * (D / 4) + kAttnThreads - 1) / kAttnThreads);
-    const dim3 jg(static_cast<unsigned>(static_cast<int64_t>(j.join_blocks) * a.n_seqs));
-    hipLaunchKernelGGL((kv4_join_kernel<D, DT>), jg, dim3(kAttnThreads), 0, stream, j);
+    int sg = 0;
+    while (sg < (D == 64 ? 4 : 3) && (2 << sg) <= a.splits) ++sg;
+    const int rows_per = kAttnThreads / (D / 4) >> sg;
+    const int64_t jb = (static_cast<int64_t>(a.max_q) * a.n_q_heads + rows_per - 1) / rows_per;
+    hipLaunchKernelGGL((kv4_join_kernel<D, DT>), dim3(static_cast<unsigned>(jb * a.n_seqs)), block, 0, stream, a,
+                       static_cast<int>(jb), sg);
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Splits of the cached tokens: enough workgroups to fill the chip, each with
-// at least two blocks per wave.
-int32_t kv4_attn_splits(int64_t workgroups, int64_t max_kv) {
-  constexpr int64_t kWant = 1024;
-  const int64_t blocks = (max_kv + kKv4Block - 1) / kKv4Block;
-  const int64_t most = (blocks + 2 * kAttnWaves - 1) / (2 * kAttnWaves);
-  const int64_t want = (kWant + workgroups - 1) / workgroups;
-  return static_cast<int32_t>(std::max<int64_t>(1, std::min(most, want)));
+int64_t kv4_attn_tile_rows(int64_t rows, int head_dim) {
+  const AttnShape s = attn_shape(rows, head_dim);
+  return s.g ? 16 / s.g : 16 * s.r * kAttnWaves;
+}
+
+// Splits of the cached tokens.  Each costs a workgroup's start and end (about
+// 4 us of latency) and a share of the join, so there are as many as fill the
+// chip and no more: two workgroups a CU, where that leaves a wave at least 4
+// chunks (few rows) or 8 blocks; and up to 1536 workgroups, for batches of
+// uneven lengths, where it leaves a wave 8 chunks.  Measured, us: one sequence of
+// 131072 tokens, 8 heads of 64: 33.9 / 22.4 / 20.6 / 22.4 / 25.1 with 16 / 32 /
+// 64 / 128 / 192 splits; 48 uneven ones, 8 heads of 128: 101 / 92 / 89 / 95 with
+// 2 / 3 / 4 / 6; a 2048-token chunk over 8192 (256 workgroups): 304 / 232 / 242
+// with 1 / 2 / 4.
+int32_t kv4_attn_splits(int64_t rows, int head_dim, int64_t workgroups, int64_t max_kv) {
+  const AttnShape s = attn_shape(rows, head_dim);
+  auto share = [&](int64_t want, int64_t unit) {  // unit: tokens of the smallest split
+    return std::min((max_kv + unit - 1) / unit, (want + workgroups - 1) / workgroups);
+  };
+  const int64_t chunk = s.g ? int64_t(kAttnWaves) * s.g * kKv4Block : kKv4Block;
+  int64_t n = s.g ? share(512, 4 * chunk) : share(512, 8 * chunk);
+  if (s.g) n = std::max(n, share(1536, 8 * chunk));
+  return static_cast<int32_t>(std::max<int64_t>(1, n));
 }
 
 hipError_t launch_kv4_attn(const AttnArgs& a, int head_dim, int dt, hipStream_t stream) {
