@@ -579,38 +579,59 @@ class GroupedGemm:
 # ---- attention on a 4-bit key/value cache ----
 
 _FP = (torch.float32, torch.float16, torch.bfloat16)
-
-
-def _same_gpu(dev, **named):
-    for name, t in named.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if dev.type != "cuda":
-        raise ValueError("tensors must be on the GPU")
+_F16 = (torch.float16, torch.bfloat16)
 
 
 def _launch(fn_name, f, dev, *args):
-    """The call on the tensors' own device and its current stream, whichever
+    """The call on device `dev` (an index) and its current stream, whichever
     device is current."""
-    if dev.index == torch.cuda.current_device():
-        status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if dev == torch._C._cuda_getDevice():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         _check(fn_name, status)
 
 
-def _check_heads_tensor(t, name, shape=None, dtypes=_FP):
-    """[tokens, heads, head_dim] with unit stride along head_dim."""
+def _gpu_of(t):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be on the GPU")
+    return dev
+
+
+def _refuse(t, name, shape, dtype, dev, layout):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise ValueError(f"{name} must be [tokens, heads, head_dim] with unit stride along head_dim")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {[str(d) for d in dtypes]}")
+    raise ValueError(f"{name} must be {layout} {dtype} {tuple(shape)} on {f'GPU {dev}' if dev >= 0 else 'the GPU'}, got "
+                     f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _heads(t, name, shape, dtype, dev):
+    """Pointer, token and head stride of t [tokens, heads, head_dim], whose unit
+    stride is along head_dim.  (Each check of a tensor's metadata costs about
+    0.1 us, and a decode step's kernels take two to five.)"""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, shape, dtype, dev, "[tokens, heads, head_dim]")
+    st, sh, sd = t.stride()
+    if sd != 1 and shape[2] > 1:
+        _refuse(t, name, shape, dtype, dev, "unit-stride (along head_dim)")
+    return t.data_ptr(), st, sh
+
+
+def _flat(t, name, shape, dtype, dev):
+    """Pointer of a contiguous tensor of this shape, type and device."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(t, name, shape, dtype, dev, "contiguous")
+    return t.data_ptr()
+
+
+def _dims(t, name, n, layout):
+    shape = t.shape
+    if len(shape) != n:
+        raise ValueError(f"{name} must be {layout}, got shape {tuple(shape)}")
+    return shape
 
 
 def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out_dtype=None,
@@ -624,42 +645,34 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e
     lie); cos, sin fp32 [max_pos, rot_dim / 2]; positions int64 [n].  The first
     rot_dim values rotate as pairs (i, i + rot_dim / 2), or (2i, 2i + 1) with
     interleaved.  q_out / k_out may be q / k themselves.  Returns (q, k)."""
-    _check_heads_tensor(q, "q")
-    n, hq, d = q.shape
-    if k is not None:
-        _check_heads_tensor(k, "k", (n, k.shape[1] if k.dim() == 3 else 0, d), (q.dtype,))
-    _need(cos, "cos", dim=2, dtypes=(torch.float32,))
-    _need(sin, "sin", dim=2, dtypes=(torch.float32,))
-    if cos.shape != sin.shape or not cos.is_contiguous() or not sin.is_contiguous():
-        raise ValueError("cos and sin must be contiguous and of one shape [max_pos, rot_dim / 2]")
-    _need(positions, "positions", numel=n, dim=1, dtypes=(torch.int64,))
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _need(w, name, numel=d, dim=1, dtypes=(torch.float32,))
-        if w is not None and not w.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    if not positions.is_contiguous():
-        raise ValueError("positions must be contiguous")
-    y_dt = out_dtype or (q_out.dtype if q_out is not None else q.dtype)
+    n, hq, d = shape = _dims(q, "q", 3, "[tokens, heads, head_dim]")
+    dev, x_dt = q.get_device(), q.dtype
+    if out_dtype is None:
+        out_dtype = x_dt if q_out is None else q_out.dtype
+    if x_dt not in _FP or out_dtype not in _FP:
+        raise ValueError(f"dtypes {x_dt} and {out_dtype}, expected {[str(t) for t in _FP]}")
+    qp, q_st, q_sh = _heads(q, "q", shape, x_dt, dev)
     if q_out is None:
-        q_out = torch.empty(n, hq, d, dtype=y_dt, device=q.device)
-    _check_heads_tensor(q_out, "q_out", q.shape, (y_dt,) if y_dt in _FP else _FP)
-    if k is not None:
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=y_dt, device=q.device)
-        _check_heads_tensor(k_out, "k_out", k.shape, (y_dt,))
-    elif k_out is not None or k_weight is not None:
-        raise ValueError("k_out and k_weight need k")
-    _same_gpu(q.device, k=k, cos=cos, sin=sin, positions=positions, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
-              k_out=k_out)
-    qs = Heads(q.data_ptr(), q_out.data_ptr(), _ptr(q_weight), q.stride(0), q.stride(1), q_out.stride(0),
-               q_out.stride(1), hq)
+        q_out = torch.empty(shape, dtype=out_dtype, device=q.device)
+    yp, y_st, y_sh = _heads(q_out, "q_out", shape, out_dtype, dev)
+    w = None if q_weight is None else _flat(q_weight, "q_weight", (d,), torch.float32, dev)
+    qs = Heads(qp, yp, w, q_st, q_sh, y_st, y_sh, hq)
     ks = None
     if k is not None:
-        ks = Heads(k.data_ptr(), k_out.data_ptr(), _ptr(k_weight), k.stride(0), k.stride(1), k_out.stride(0),
-                   k_out.stride(1), k.shape[1])
-    _launch("sherry_qk_norm_rope", load().sherry_qk_norm_rope, q.device, qs, ks, _DT[q.dtype], _DT[y_dt], n, d,
-            2 * cos.shape[1], int(bool(interleaved)), cos.data_ptr(), sin.data_ptr(), cos.shape[0],
-            positions.data_ptr(), eps)
+        k_shape = (n, _dims(k, "k", 3, "[tokens, heads, head_dim]")[1], d)
+        kp, k_st, k_sh = _heads(k, "k", k_shape, x_dt, dev)
+        if k_out is None:
+            k_out = torch.empty(k_shape, dtype=out_dtype, device=q.device)
+        yp, y_st, y_sh = _heads(k_out, "k_out", k_shape, out_dtype, dev)
+        w = None if k_weight is None else _flat(k_weight, "k_weight", (d,), torch.float32, dev)
+        ks = Heads(kp, yp, w, k_st, k_sh, y_st, y_sh, k_shape[1])
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    max_pos, half = table = _dims(cos, "cos", 2, "[max_pos, rot_dim / 2]")
+    cp, sp = _flat(cos, "cos", table, torch.float32, dev), _flat(sin, "sin", table, torch.float32, dev)
+    pp = _flat(positions, "positions", (n,), torch.int64, dev)
+    _launch("sherry_qk_norm_rope", (_lib or load()).sherry_qk_norm_rope, _gpu_of(q), qs, ks, _DT[x_dt], _DT[out_dtype], n,
+            d, 2 * half, 1 if interleaved else 0, cp, sp, max_pos, pp, eps)
     return q_out, k_out
 
 
@@ -677,47 +690,51 @@ class Kv4Cache:
         _need(data, "data", dtypes=(torch.uint8,), min_nbytes=nbytes)
         if not data.is_contiguous():
             raise ValueError("data must be contiguous")
-        self.data, self.nbytes = data, nbytes
+        self.data, self.nbytes, self.device = data, nbytes, data.get_device()
         self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
         self.desc = Kv4CacheDesc(data.data_ptr(), n_pages, page_size, n_kv_heads, head_dim)
 
 
-def _check_slots(slots):
-    _need(slots, "slots", dim=1, dtypes=(torch.int64,))
-    if not slots.is_contiguous():
-        raise ValueError("slots must be contiguous")
-    return slots.numel()
+def _slots(slots, dev):
+    shape = _dims(slots, "slots", 1, "[n]")
+    return shape[0], _flat(slots, "slots", shape, torch.int64, dev)
 
 
 def kv4_write(cache, k, v, slots):
     """Quantise k, v [n, kv_heads, head_dim] (fp32, fp16 or bf16, any token and
     head strides) into the cache at slots (int64 [n], page * page_size + place,
     all different; one outside the cache is skipped) (sherry_kv4_write)."""
-    shape = (_check_slots(slots), cache.n_kv_heads, cache.head_dim)
-    _check_heads_tensor(k, "k", shape)
-    _check_heads_tensor(v, "v", shape, (k.dtype,))
-    _same_gpu(cache.data.device, k=k, v=v, slots=slots)
-    _launch("sherry_kv4_write", load().sherry_kv4_write, cache.data.device, cache.desc, k.data_ptr(), v.data_ptr(),
-            _DT[k.dtype], shape[0], k.stride(0), k.stride(1), v.stride(0), v.stride(1), slots.data_ptr())
+    dev = cache.device
+    n, sp = _slots(slots, dev)
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    dt = k.dtype
+    if dt not in _FP:
+        raise ValueError(f"k has dtype {dt}, expected one of {[str(t) for t in _FP]}")
+    kp, k_st, k_sh = _heads(k, "k", shape, dt, dev)
+    vp, v_st, v_sh = _heads(v, "v", shape, dt, dev)
+    _launch("sherry_kv4_write", (_lib or load()).sherry_kv4_write, _gpu_of(k), cache.desc, kp, vp, _DT[dt], n, k_st,
+            k_sh, v_st, v_sh, sp)
 
 
 def kv4_read(cache, slots, out_dtype=torch.float16, k_out=None, v_out=None):
     """The values that the cache holds at slots (int64 [n]) as k, v
     [n, kv_heads, head_dim]; slots outside the cache read as zeros
     (sherry_kv4_read)."""
-    shape = (_check_slots(slots), cache.n_kv_heads, cache.head_dim)
+    dev = cache.device
+    n, sp = _slots(slots, dev)
+    shape = (n, cache.n_kv_heads, cache.head_dim)
     if k_out is not None or v_out is not None:
         out_dtype = (k_out if k_out is not None else v_out).dtype
     if k_out is None:
         k_out = torch.empty(shape, dtype=out_dtype, device=cache.data.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=out_dtype, device=cache.data.device)
-    _check_heads_tensor(k_out, "k_out", shape)
-    _check_heads_tensor(v_out, "v_out", shape, (k_out.dtype,))
-    _same_gpu(cache.data.device, slots=slots, k_out=k_out, v_out=v_out)
-    _launch("sherry_kv4_read", load().sherry_kv4_read, cache.data.device, cache.desc, k_out.data_ptr(),
-            v_out.data_ptr(), _DT[k_out.dtype], shape[0], k_out.stride(0), k_out.stride(1), v_out.stride(0),
-            v_out.stride(1), slots.data_ptr())
+    if out_dtype not in _FP:
+        raise ValueError(f"out_dtype {out_dtype}, expected one of {[str(t) for t in _FP]}")
+    kp, k_st, k_sh = _heads(k_out, "k_out", shape, out_dtype, dev)
+    vp, v_st, v_sh = _heads(v_out, "v_out", shape, out_dtype, dev)
+    _launch("sherry_kv4_read", (_lib or load()).sherry_kv4_read, _gpu_of(slots), cache.desc, kp, vp, _DT[out_dtype], n,
+            k_st, k_sh, v_st, v_sh, sp)
     return k_out, v_out
 
 
@@ -738,37 +755,33 @@ def kv4_attn(cache, q, page_table, kv_lens, cu_q=None, max_q=1, max_kv=None, sca
     the new tokens of a sequence, max_kv (default: what the table holds) sizes
     the launch, scale defaults to head_dim ** -0.5.  A row that sees nothing is
     zeros.  Returns (out, lse fp32 [n, heads] or None)."""
-    _check_heads_tensor(q, "q", dtypes=(torch.float16, torch.bfloat16))
-    n, hq, d = q.shape
-    if d != cache.head_dim:
-        raise ValueError(f"q has head_dim {d}, the cache {cache.head_dim}")
-    _need(page_table, "page_table", dim=2, dtypes=(torch.int32,))
-    n_seqs, width = page_table.shape
-    if width > 1 and page_table.stride(1) != 1:
-        raise ValueError("page_table must have unit stride along its rows")
-    _need(kv_lens, "kv_lens", numel=n_seqs, dim=1, dtypes=(torch.int32,))
-    _need(cu_q, "cu_q", numel=n_seqs + 1, dim=1, dtypes=(torch.int32,))
-    if not kv_lens.is_contiguous() or (cu_q is not None and not cu_q.is_contiguous()):
-        raise ValueError("kv_lens and cu_q must be contiguous")
+    dev = cache.device
+    n, hq, d = shape = _dims(q, "q", 3, "[tokens, heads, head_dim]")
+    dt = q.dtype
+    if d != cache.head_dim or dt not in _F16:
+        raise ValueError(f"q has head_dim {d} and dtype {dt}, expected {cache.head_dim} and one of "
+                         f"{[str(t) for t in _F16]}")
+    qp, q_st, q_sh = _heads(q, "q", shape, dt, dev)
     if out is None:
-        out = torch.empty(n, hq, d, dtype=q.dtype, device=q.device)
-    _check_heads_tensor(out, "out", q.shape, (q.dtype,))
+        out = torch.empty(shape, dtype=dt, device=q.device)
+    op, o_st, o_sh = _heads(out, "out", shape, dt, dev)
+    n_seqs, width = t_shape = _dims(page_table, "page_table", 2, "[n_seqs, width]")
+    t_st, t_sd = page_table.stride()
+    if page_table.dtype is not torch.int32 or page_table.get_device() != dev or (t_sd != 1 and width > 1):
+        _refuse(page_table, "page_table", t_shape, torch.int32, dev, "unit-stride (along its rows)")
+    lp = _flat(kv_lens, "kv_lens", (n_seqs,), torch.int32, dev)
+    cp = None if cu_q is None else _flat(cu_q, "cu_q", (n_seqs + 1,), torch.int32, dev)
     if lse is None and want_lse:
         lse = torch.empty(n, hq, dtype=torch.float32, device=q.device)
-    _need(lse, "lse", dim=2, dtypes=(torch.float32,))
-    if lse is not None and (tuple(lse.shape) != (n, hq) or not lse.is_contiguous()):
-        raise ValueError(f"lse must be contiguous [{n}, {hq}], got shape {tuple(lse.shape)}")
+    sp = None if lse is None else _flat(lse, "lse", (n, hq), torch.float32, dev)
     if max_kv is None:
         max_kv = width * cache.page_size
     if workspace is None:
         workspace = kv4_attn_workspace(cache, n, hq, n_seqs, max_q, max_kv)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _same_gpu(cache.data.device, q=q, page_table=page_table, kv_lens=kv_lens, cu_q=cu_q, out=out, lse=lse,
-              workspace=workspace)
-    _launch("sherry_kv4_attn", load().sherry_kv4_attn, q.device, cache.desc, q.data_ptr(), _DT[q.dtype], n, hq,
-            q.stride(0), q.stride(1), _ptr(cu_q), n_seqs, max_q, max_kv, page_table.data_ptr(), width,
-            page_table.stride(0), kv_lens.data_ptr(), scale if scale is not None else d ** -0.5,
-            out.data_ptr(), out.stride(0), out.stride(1), _ptr(lse), workspace.data_ptr() or None,
-            workspace.numel() * workspace.element_size())
+    ws_bytes = workspace.numel() * workspace.element_size()
+    if not workspace.is_contiguous() or (workspace.get_device() != dev and ws_bytes):
+        raise ValueError("workspace must be contiguous and on the cache's device")
+    _launch("sherry_kv4_attn", (_lib or load()).sherry_kv4_attn, _gpu_of(q), cache.desc, qp, _DT[dt], n, hq, q_st, q_sh,
+            cp, n_seqs, max_q, max_kv, page_table.data_ptr(), width, t_st, lp, d ** -0.5 if scale is None else scale, op,
+            o_st, o_sh, sp, workspace.data_ptr() or None, ws_bytes)
     return out, lse
