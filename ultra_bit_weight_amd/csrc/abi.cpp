@@ -553,7 +553,7 @@ sherry_status attn_sizes(const sherry_kv4_cache* cache, int64_t n_tokens, int32_
   const int64_t rows = static_cast<int64_t>(max_q) * a->group;
   if (rows > kMaxDim / 256) return SHERRY_ESHAPE;
   const int64_t tile = kv4_attn_tile_rows(rows, cache->head_dim), tiles = (rows + tile - 1) / tile;
-  if (tiles * n_seqs > kMaxDim / 256) return SHERRY_ESHAPE;  // threads of the launch
+  if (tiles * n_seqs > kMaxDim / 256 / a->c.n_kv_heads) return SHERRY_ESHAPE;  // threads of the launch
   a->row_tiles = static_cast<int32_t>(tiles);
   a->splits = kv4_attn_splits(rows, cache->head_dim, tiles * n_seqs * a->c.n_kv_heads, max_kv);
   *workspace = a->splits == 1 ? 0 : static_cast<size_t>(a->splits) * n_tokens * n_q_heads * (cache->head_dim + 2) * 4;

@@ -98,6 +98,24 @@ __device__ __forceinline__ SeqRange seq_range(const AttnArgs& a, int s) {
   return r;
 }
 
+// A workgroup's share of the call.  Key heads vary fastest (with 8 of them, each
+// XCD keeps one head's blocks in its L2), then splits, sequences, and row tiles
+// from the last: the last rows see most tokens, and start first.
+struct Place {
+  int tile, seq, split, head;
+};
+__device__ __forceinline__ Place place(const AttnArgs& a) {
+  Place p;
+  int i = static_cast<int>(blockIdx.x);
+  p.head = i % a.c.n_kv_heads;
+  i /= a.c.n_kv_heads;
+  p.split = i % a.splits;
+  i /= a.splits;
+  p.seq = i % a.n_seqs;
+  p.tile = a.row_tiles - 1 - i / a.n_seqs;
+  return p;
+}
+
 // Operands made of a pair of dwords: K (low or high nibbles) and V.
 template <bool kHigh>
 __device__ __forceinline__ half8_t k_operand(uint32_t w0, uint32_t w1) {
@@ -372,11 +390,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
   __shared__ float lds_o[kAttnWaves][16][kPad];
   __shared__ float lds_m[kAttnWaves][16], lds_l[kAttnWaves][16];
 
-  const int split = static_cast<int>(blockIdx.x % a.splits);
-  const int st_id = static_cast<int>(blockIdx.x / a.splits);
-  const int seq = st_id / a.row_tiles;
-  const int row0 = (st_id - seq * a.row_tiles) * kRows;
-  const int kvh = blockIdx.y;
+  const Place at_place = place(a);
+  const int split = at_place.split, seq = at_place.seq, kvh = at_place.head;
+  const int row0 = at_place.tile * kRows;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x & (kWave - 1);
   const int col = lane & 15, g = lane >> 4;
@@ -585,17 +601,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
   // the queries of two tiles at D = 128 would not fit the registers of two waves
   constexpr bool kLdsQ = D == 128 && R > 1;
   __shared__ u32x4_t lds_q[kLdsQ ? kAttnWaves : 1][kLdsQ ? R : 1][kLdsQ ? KS : 1][kWave];
-  const int split = static_cast<int>(blockIdx.x % a.splits);
-  const int st_id = static_cast<int>(blockIdx.x / a.splits);
-  const int seq = st_id / a.row_tiles;
-  const int kvh = blockIdx.y;
+  const Place at_place = place(a);
+  const int split = at_place.split, seq = at_place.seq, kvh = at_place.head;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x & (kWave - 1);
   const int col = lane & 15, g = lane >> 4;
   const SeqRange sr = seq_range(a, seq);
   const int rows = min(sr.n, a.max_q) * a.group;
-  // the last rows see most tokens: they start first
-  const int wg0 = (a.row_tiles - 1 - (st_id - seq * a.row_tiles)) * kRows;
+  const int wg0 = at_place.tile * kRows;
   if (wg0 >= rows) return;
   const int row0 = wg0 + wave * 16 * R;
   const bool has_rows = row0 < rows;  // a wave without rows still unpacks
@@ -842,8 +855,7 @@ AttnShape attn_shape(int64_t rows, int head_dim) {
 
 template <int D, int DT>
 hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.splits) * a.n_seqs * a.row_tiles),
-                  static_cast<unsigned>(a.c.n_kv_heads));
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.splits) * a.n_seqs * a.row_tiles * a.c.n_kv_heads));
   const AttnShape s = attn_shape(static_cast<int64_t>(a.max_q) * a.group, D);
   const dim3 block(kAttnThreads);
   if (s.g == 2) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 2>), grid, block, 0, stream, a);
