@@ -555,7 +555,8 @@ sherry_status attn_sizes(const sherry_kv4_cache* cache, int64_t n_tokens, int32_
   const int64_t tile = kv4_attn_tile_rows(rows, cache->head_dim), tiles = (rows + tile - 1) / tile;
   if (tiles * n_seqs > kMaxDim / 256 / a->c.n_kv_heads) return SHERRY_ESHAPE;  // threads of the launch
   a->row_tiles = static_cast<int32_t>(tiles);
-  a->splits = kv4_attn_splits(rows, cache->head_dim, tiles * n_seqs * a->c.n_kv_heads, max_kv);
+  a->splits = kv4_attn_splits(rows, cache->head_dim, tiles * n_seqs * a->c.n_kv_heads,
+                              std::min(max_kv, int64_t(1) << 30));
   *workspace = a->splits == 1 ? 0 : static_cast<size_t>(a->splits) * n_tokens * n_q_heads * (cache->head_dim + 2) * 4;
   return SHERRY_OK;
 }
@@ -603,6 +604,10 @@ sherry_status kv4_attn_impl(const sherry_kv4_cache* cache, const void* q, dt_t d
   a.table_stride = table_stride;
   a.table_width = table_width;
   a.scale = scale;
+  a.by_kv_heads = FastDiv(static_cast<uint32_t>(a.c.n_kv_heads));
+  a.by_splits = FastDiv(static_cast<uint32_t>(a.splits));
+  a.by_seqs = FastDiv(static_cast<uint32_t>(a.n_seqs));
+  a.by_group = FastDiv(static_cast<uint32_t>(a.group));
   return launched(launch_kv4_attn(a, cache->head_dim, act_dt(dt), stream));
 }
 

@@ -82,19 +82,22 @@ struct SeqRange {
   int32_t len;    // cached tokens, new ones included
 };
 
+// New tokens only (len 0).  (Loads before any branch, so that they and the
+// lengths' go out together.)
+__device__ __forceinline__ SeqRange new_range(const AttnArgs& a, int s) {
+  const SHERRY_GLOBAL int32_t* cu = gmem(a.cu_q ? a.cu_q : a.kv_lens);
+  const int64_t from = cu[s], to = cu[a.cu_q ? s + 1 : s];
+  const int64_t b = min(max(from, int64_t(0)), a.n_tokens);
+  const int64_t e = min(max(to, b), a.n_tokens);
+  return a.cu_q ? SeqRange{b, static_cast<int32_t>(e - b), 0}
+                : SeqRange{static_cast<int64_t>(s) * a.max_q, a.max_q, 0};
+}
+
 __device__ __forceinline__ SeqRange seq_range(const AttnArgs& a, int s) {
-  SeqRange r;
-  if (a.cu_q) {
-    const int64_t b = min(max(static_cast<int64_t>(gmem(a.cu_q)[s]), int64_t(0)), a.n_tokens);
-    const int64_t e = min(max(static_cast<int64_t>(gmem(a.cu_q)[s + 1]), b), a.n_tokens);
-    r.first = b;
-    r.n = static_cast<int32_t>(e - b);
-  } else {
-    r.first = static_cast<int64_t>(s) * a.max_q;
-    r.n = a.max_q;
-  }
+  const int32_t len = gmem(a.kv_lens)[s];
+  SeqRange r = new_range(a, s);
   const int64_t cap = static_cast<int64_t>(a.table_width) << a.c.page_shift;
-  r.len = static_cast<int32_t>(min(static_cast<int64_t>(max(gmem(a.kv_lens)[s], 0)), cap));
+  r.len = static_cast<int32_t>(min(static_cast<int64_t>(max(len, 0)), cap));
   return r;
 }
 
@@ -107,12 +110,13 @@ struct Place {
 __device__ __forceinline__ Place place(const AttnArgs& a) {
   Place p;
   int i = static_cast<int>(blockIdx.x);
-  p.head = i % a.c.n_kv_heads;
-  i /= a.c.n_kv_heads;
-  p.split = i % a.splits;
-  i /= a.splits;
-  p.seq = i % a.n_seqs;
-  p.tile = a.row_tiles - 1 - i / a.n_seqs;
+  const int by_head = a.by_kv_heads(i);
+  p.head = i - by_head * a.c.n_kv_heads;
+  i = a.by_splits(by_head);
+  p.split = by_head - i * a.splits;
+  const int back = a.by_seqs(i);
+  p.seq = i - back * a.n_seqs;
+  p.tile = a.row_tiles - 1 - back;
   return p;
 }
 
@@ -403,10 +407,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
   const int nrow = min(kRows, rows - row0);
 
   // row r sees tokens below lim(r)
-  const int lim_lo = max(sr.len - sr.n + row0 / a.group + 1, 0);
-  const int lim_hi = max(min(sr.len - sr.n + (row0 + nrow - 1) / a.group + 1, sr.len), 0);
+  const int lim_lo = max(sr.len - sr.n + a.by_group(row0) + 1, 0);
+  const int lim_hi = max(min(sr.len - sr.n + a.by_group(row0 + nrow - 1) + 1, sr.len), 0);
   const int row = min(row0 + col % kRows, rows - 1);
-  const int tok = row / a.group;
+  const int tok = a.by_group(row);
   const int head = kvh * a.group + (row - tok * a.group);
   const int lim = sr.len - sr.n + tok + 1;
 
@@ -572,7 +576,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = __builtin_fmaf(f, t[j], o[j]);
     }
-    const int rr = row0 + r, ti = rr / a.group;
+    const int rr = row0 + r, ti = a.by_group(rr);
     store_row<D, DT>(a, split, sr.first + ti, kvh * a.group + (rr - ti * a.group), d, o, m, l);
   }
 }
@@ -612,7 +616,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
   if (wg0 >= rows) return;
   const int row0 = wg0 + wave * 16 * R;
   const bool has_rows = row0 < rows;  // a wave without rows still unpacks
-  auto limit = [&](int row) { return max(min(sr.len - sr.n + row / a.group + 1, sr.len), 0); };
+  auto limit = [&](int row) { return max(min(sr.len - sr.n + a.by_group(row) + 1, sr.len), 0); };
   const int lim_lo = limit(wg0), lim_hi = limit(min(wg0 + kRows, rows) - 1);
   const int wave_hi = limit(min(row0 + 16 * R, rows) - 1);
 
@@ -680,7 +684,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int row = min(row0 + 16 * r + col, rows - 1);
-      const int tok = row / a.group, head = kvh * a.group + (row - tok * a.group);
+      const int tok = a.by_group(row), head = kvh * a.group + (row - tok * a.group);
       lim[r] = sr.len - sr.n + tok + 1;
       f[r].load(a.q, (sr.first + tok) * a.q_st + head * a.q_sh + 8 * g);
       top = fmaxf(top, f[r].top());
@@ -765,7 +769,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
     acc[r].finish();
     const int row = row0 + 16 * r + col;
     if (row >= rows) continue;
-    const int tok = row / a.group, head = kvh * a.group + (row - tok * a.group);
+    const int tok = a.by_group(row), head = kvh * a.group + (row - tok * a.group);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       float o[4];
@@ -777,15 +781,15 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
 }
 
 // Joins the splits of every row.  A row takes D / 4 lanes (four values each)
-// times 1 << sg_shift groups, and group i the splits i, i + groups, ...: first
-// the largest maximum, then the sums, so that no load waits for another.
+// times 1 << sg_shift groups, and group i the splits i, i + groups, ..., four at a
+// time, so that one latency covers up to 64 (D = 64) or 32 of them.
 template <int D, int DT>
 __global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(AttnArgs a, int join_blocks, int sg_shift) {
   constexpr int kLanes = D / 4;
   __shared__ f32x4_t lds_o[kAttnThreads];
   __shared__ f32x2_t lds_ml[kAttnThreads];
   const int seq = static_cast<int>(blockIdx.x / join_blocks);
-  const SeqRange sr = seq_range(a, seq);
+  const SeqRange sr = new_range(a, seq);
   const int groups = 1 << sg_shift;
   const int lane = threadIdx.x % kLanes;
   const int grp = (threadIdx.x / kLanes) & (groups - 1);
@@ -802,16 +806,28 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(AttnArgs a, int 
   if (live) {
     const SHERRY_GLOBAL f32x2_t* ml = gmem(reinterpret_cast<const f32x2_t*>(a.part_ml)) + at;
     const SHERRY_GLOBAL f32x4_t* po = gmem(reinterpret_cast<const f32x4_t*>(a.part_o)) + at * kLanes + lane;
-#pragma unroll 4
-    for (int s = grp; s < a.splits; s += groups) m = fmaxf(m, ml[s * step].x);
-#pragma unroll 4
-    for (int s = grp; s < a.splits; s += groups) {
-      const f32x2_t t = ml[s * step];
-      const f32x4_t o = po[s * step * kLanes];
-      const float f = __builtin_amdgcn_exp2f(t.x - m);
-      l = __builtin_fmaf(f, t.y, l);
+    for (int s0 = grp; s0 < a.splits; s0 += 4 * groups) {
+      f32x2_t t[4];
+      f32x4_t o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(f, o[j], v[j]);
+      for (int i = 0; i < 4; ++i) {  // (past the last: the first again, with no weight)
+        const int s = s0 + i * groups < a.splits ? s0 + i * groups : s0;
+        t[i] = ml[s * step];
+        o[i] = po[s * step * kLanes];
+      }
+      const float m_old = m;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, t[i].x);
+      const float keep = __builtin_amdgcn_exp2f(m_old - m);
+      l *= keep;
+      v *= keep;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = s0 + i * groups < a.splits ? __builtin_amdgcn_exp2f(t[i].x - m) : 0.0f;
+        l = __builtin_fmaf(f, t[i].y, l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(f, o[i][j], v[j]);
+      }
     }
   }
   if (groups > 1) {

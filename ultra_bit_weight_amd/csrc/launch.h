@@ -285,8 +285,23 @@ struct Kv4Rows {
 };
 hipError_t launch_kv4_rows(const Kv4Geom& g, int head_dim, const Kv4Rows& r, int dt, bool write, hipStream_t stream);
 
+// n / d for 0 <= n < 2^31 by a multiplication: the quotient is
+// (hi32(n mul) + n) >> shift with shift = ceil(log2 d) and
+// mul = floor(2^32 (2^shift - d) / d) + 1.
+struct FastDiv {
+  uint32_t mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) : mul(0), shift(0) {
+    while ((uint64_t(1) << shift) < d) ++shift;
+    mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+};
 struct AttnArgs {
   Kv4Geom c;
+  FastDiv by_kv_heads, by_splits, by_seqs, by_group;
   const void* q;
   void* out;
   float* lse;             // nullable
