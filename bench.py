@@ -57,6 +57,10 @@ def parse_args(argv=None):
     p.add_argument("--f4-profile", action="store_true",
                    help="only the decode pipeline (a 1B token's fused products over min(16, replicas) layers, "
                         "eager and graph replay); prints its timing and exits")
+    p.add_argument("--f4-attention", type=int, default=0, metavar="TOKENS",
+                   help="only the decode pipeline with its attention run: per layer the rotation, the write to a "
+                        "4-bit cache of its own and attention over TOKENS cached tokens between the q|k|v and o "
+                        "products; eager and graph replay, prints its timing and exits")
     p.add_argument("--bf16-gemm-profile", action="store_true",
                    help="only the grouped bf16 few-token GEMM on the 3B layer (M = 2, 4, 8, 16) over 72 replicas; "
                         "prints their rates and exits")
@@ -587,6 +591,65 @@ def f4_decode_token(torch, sherry, probs, layers):
     return res
 
 
+def f4_decode_token_attention(torch, sherry, probs, layers, tokens, steps=50):
+    """The 1B token of f4_decode_token with its attention: per layer q|k|v
+    product, rotation of q and k, the new token's keys and values into a 4-bit
+    cache, attention of its 32 heads over `tokens` cached tokens (8 key heads of
+    64), o product on its output, gate|up and down.  Every layer has weights
+    and a cache of its own.  Timed eager and replayed from one HIP graph
+    (checked against eager first)."""
+    dev = torch.device("cuda:0")
+    hq, hkv, d, page = 32, 8, 64, 64
+    pages = -(-tokens // page)
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(4)
+    ang = torch.arange(tokens, dtype=torch.float64, device=dev)[:, None] * \
+        500000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64, device=dev) / d)
+    cos, sin = ang.cos().float(), ang.sin().float()
+    pos = torch.tensor([tokens - 1], device=dev)
+    lens = torch.tensor([tokens], dtype=torch.int32, device=dev)
+    f16 = dict(dtype=torch.float16, device=dev)
+    parts, outs = [], []
+    for l in range(layers):
+        by = {p["name"]: p for p in probs if p["replica"] == l}
+
+        def product(names, x, by=by):
+            y = torch.empty(sum(by[nm]["n"] for nm in names), **f16)
+            return sherry.PreparedGemvQuant(torch.cat([by[nm]["codes"] for nm in names]),
+                                            torch.cat([by[nm]["scales"] for nm in names]), x, out=y)
+        cache = sherry.Kv4Cache(pages, page, hkv, d, device=dev)
+        table = torch.randperm(pages, generator=gen, device=dev).to(torch.int32).view(1, pages)
+        every = (table[0].long()[:, None] * page + torch.arange(page, device=dev)).flatten()[:tokens]
+        sherry.kv4_write(cache, *(torch.randn(tokens, hkv, d, generator=gen, device=dev).half() for _ in range(2)), every)
+        qkv = product(("q", "k", "v"), torch.randn(2048, generator=gen, device=dev).to(torch.bfloat16))
+        heads = qkv.y.view(1, hq + 2 * hkv, d)
+        q, k, att = torch.empty(1, hq, d, **f16), torch.empty(1, hkv, d, **f16), torch.empty(1, hq, d, **f16)
+        o = product(("o",), att.view(-1))
+        gu = product(("gate", "up"), torch.randn(2048, generator=gen, device=dev).to(torch.bfloat16))
+        down = product(("down",), torch.randn(8192, generator=gen, device=dev).to(torch.bfloat16))
+        ws = sherry.kv4_attn_workspace(cache, 1, hq, 1, 1, tokens)
+        parts.append((qkv, heads, q, k, every[tokens - 1:], cache, table, att, ws, o, gu, down))
+        outs += [q, k, att, o.y, gu.y, down.y]
+
+    def token():
+        for qkv, heads, q, k, slot, cache, table, att, ws, o, gu, down in parts:
+            qkv()
+            sherry.qk_norm_rope(heads[:, :hq], heads[:, hq:hq + hkv], cos, sin, pos, q_out=q, k_out=k)
+            sherry.kv4_write(cache, k, heads[:, hq + hkv:], slot)
+            sherry.kv4_attn(cache, q, table, lens, max_kv=tokens, out=att, workspace=ws)
+            o()
+            gu()
+            down()
+    res = {"layers": layers, "cached_tokens": tokens, "cache_bytes_per_token": layers * tokens * hkv * (d + 8 * (d // 64))}
+    mean_ms, _ = time_launches(torch, token, steps, 5)
+    res["eager_us_per_token"] = round(mean_ms * 1e3, 1)
+    gus = graph_time(torch, token, outs, replays=steps)
+    res["graph_us_per_token"] = gus
+    if isinstance(gus, float):
+        res["graph_us_per_layer"] = round(gus / layers, 2)
+    return res
+
+
 def graph_time(torch, fn, outs, replays=200):
     """Mean us per replay of fn captured in a HIP graph, after checking three
     replays (outputs cleared before each) against one eager run; a string
@@ -986,6 +1049,9 @@ def main(argv=None):
         return gemm_profile(torch, sherry, synth, probs, args)
     if args.f4_profile:
         print(json.dumps(f4_decode_token(torch, sherry, probs, min(16, R))), flush=True)
+        return 0
+    if args.f4_attention > 0:
+        print(json.dumps(f4_decode_token_attention(torch, sherry, probs, min(16, R), args.f4_attention)), flush=True)
         return 0
     grouped = sherry.GroupedGemv(probs)
     torch.cuda.synchronize()

@@ -615,3 +615,16 @@ def test_two_streams_with_a_workspace_each(gpu_lib):
     for i in range(2):
         for o, lse in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_decode_pipeline_with_attention(gpu_lib):
+    """The benchmark's decode pipeline with its attention run: its graph replays
+    what its eager run gives (graph_time checks every output)."""
+    import bench
+    import synth
+
+    say("decode pipeline with attention")
+    _, probs = bench.build_layer_replicas(torch, gpu_lib, synth, synth.LLAMA32_1B_LAYER, 1, 2)
+    res = bench.f4_decode_token_attention(torch, gpu_lib, probs, 1, 100, steps=3)
+    assert res["layers"] == 1 and res["cached_tokens"] == 100 and res["eager_us_per_token"] > 0
+    assert isinstance(res["graph_us_per_token"], float), res
