@@ -3,7 +3,8 @@
     python -m ultra_bit_weight_amd.build
 
 Objects go to ultra_bit_weight_amd/_build/, the library to
-ultra_bit_weight_amd/lib/libsherry.so (written atomically).
+ultra_bit_weight_amd/lib/libsherry.so and the checks of the attention entry
+points (csrc/bind.cpp, host code) to lib/_sherry_bind.so (written atomically).
 """
 from __future__ import annotations
 
@@ -20,6 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libsherry.so")
+BIND = os.path.join(LIBDIR, "_sherry_bind.so")
 SOURCES = ["abi.cpp", "pack.hip", "gemv.hip", "gemm.hip", "gemm_bf16.hip", "gemm_prefill.hip", "gemm_tile32.hip", "act.hip", "rope.hip", "kv4.hip",
            "kv4_attn.hip", "probes.hip"]
 ARCH = "gfx950"
@@ -64,6 +66,26 @@ def _compile(src: str, save_temps: bool, objdir: str, defines) -> str:
     return obj
 
 
+def build_bind(out: str = BIND) -> str:
+    """Compile csrc/bind.cpp against the installed torch (host code only)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    tmp = out + ".tmp"
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    incs = [INCLUDE, "/opt/rocm/include", sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *[f"-isystem{i}" for i in incs],
+           os.path.join(CSRC, "bind.cpp"), "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 def build(verbose: bool = False, save_temps: bool = False, defines=(), out: str = LIB) -> str:
     """Compile every source and link `out` (default: the in-tree library).
     `defines` (NAME=VALUE strings) override the build-time tunables."""
@@ -72,8 +94,11 @@ def build(verbose: bool = False, save_temps: bool = False, defines=(), out: str 
     os.makedirs(objdir, exist_ok=True)
     os.makedirs(os.path.dirname(out), exist_ok=True)
     srcs = list(SOURCES)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        bind = ex.submit(build_bind) if out == LIB else None
         objs = list(ex.map(lambda s: _compile(s, save_temps, objdir, defines), srcs))
+    if bind:
+        bind.result()
     tmp = out + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

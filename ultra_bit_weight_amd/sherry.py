@@ -1,4 +1,5 @@
-"""Thin ctypes binding over libsherry.so (C ABI in include/sherry.h).
+"""Thin binding over libsherry.so (C ABI in include/sherry.h): ctypes, and for the
+attention entry points the same checks in C++ (csrc/bind.cpp).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of libsherry.so.  Tensors are torch tensors on the current HIP device;
@@ -9,6 +10,7 @@ raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -68,15 +70,19 @@ class Kv4CacheDesc(ctypes.Structure):
 
 
 _lib = None
+_bind = None
+_BIND_PATH = os.path.join(_HERE, "lib", "_sherry_bind.so")
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Load libsherry.so (after torch, so it binds to torch's HIP runtime)."""
-    global _lib
+    """Load libsherry.so (after torch, so it binds to torch's HIP runtime), and
+    the checks of the attention entry points (csrc/bind.cpp) over it."""
+    global _lib, _bind
     if _lib is not None:
         return _lib
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is not built; run `python -c 'import __graft_entry__ as g; g.build()'`")
+    for need in (path, _BIND_PATH):
+        if not os.path.exists(need):
+            raise RuntimeError(f"{need} is not built; run `python -c 'import __graft_entry__ as g; g.build()'`")
     lib = ctypes.CDLL(path)
     vp, i64, i32, i = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
     sz = ctypes.c_size_t
@@ -149,7 +155,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                     vp, vp, sz, vp]
     lib.sherry_set_prefill_kernel.restype = i
     lib.sherry_set_prefill_kernel.argtypes = [i]
-    _lib = lib
+    spec = importlib.util.spec_from_file_location("_sherry_bind", _BIND_PATH)
+    bind = importlib.util.module_from_spec(spec)
+    bind.attach(os.path.abspath(path))
+    _lib, _bind = lib, bind
     return lib
 
 
@@ -578,60 +587,21 @@ class GroupedGemm:
 
 # ---- attention on a 4-bit key/value cache ----
 
-_FP = (torch.float32, torch.float16, torch.bfloat16)
-_F16 = (torch.float16, torch.bfloat16)
-
-
-def _launch(fn_name, f, dev, *args):
+def _launch(fn_name, dev, *args):
     """The call on device `dev` (an index) and its current stream, whichever
-    device is current."""
-    if dev == torch._C._cuda_getDevice():
+    device is current.  csrc/bind.cpp checks the tensors and calls the C ABI."""
+    if _bind is None:
+        load()
+    f = getattr(_bind, fn_name)
+    if dev < 0:  # refused there, after what else is wrong
+        status = f(*args, 0)
+    elif dev == torch._C._cuda_getDevice():
         status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
             status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status:
-        _check(fn_name, status)
-
-
-def _gpu_of(t):
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be on the GPU")
-    return dev
-
-
-def _refuse(t, name, shape, dtype, dev, layout):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    raise ValueError(f"{name} must be {layout} {dtype} {tuple(shape)} on {f'GPU {dev}' if dev >= 0 else 'the GPU'}, got "
-                     f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-
-
-def _heads(t, name, shape, dtype, dev):
-    """Pointer, token and head stride of t [tokens, heads, head_dim], whose unit
-    stride is along head_dim.  (Each check of a tensor's metadata costs about
-    0.1 us, and a decode step's kernels take two to five.)"""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
-        _refuse(t, name, shape, dtype, dev, "[tokens, heads, head_dim]")
-    st, sh, sd = t.stride()
-    if sd != 1 and shape[2] > 1:
-        _refuse(t, name, shape, dtype, dev, "unit-stride (along head_dim)")
-    return t.data_ptr(), st, sh
-
-
-def _flat(t, name, shape, dtype, dev):
-    """Pointer of a contiguous tensor of this shape, type and device."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != dev:
-        _refuse(t, name, shape, dtype, dev, "contiguous")
-    return t.data_ptr()
-
-
-def _dims(t, name, n, layout):
-    shape = t.shape
-    if len(shape) != n:
-        raise ValueError(f"{name} must be {layout}, got shape {tuple(shape)}")
-    return shape
+        _check("sherry_" + fn_name, status)
 
 
 def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out_dtype=None,
@@ -645,34 +615,15 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e
     lie); cos, sin fp32 [max_pos, rot_dim / 2]; positions int64 [n].  The first
     rot_dim values rotate as pairs (i, i + rot_dim / 2), or (2i, 2i + 1) with
     interleaved.  q_out / k_out may be q / k themselves.  Returns (q, k)."""
-    n, hq, d = shape = _dims(q, "q", 3, "[tokens, heads, head_dim]")
-    dev, x_dt = q.get_device(), q.dtype
     if out_dtype is None:
-        out_dtype = x_dt if q_out is None else q_out.dtype
-    if x_dt not in _FP or out_dtype not in _FP:
-        raise ValueError(f"dtypes {x_dt} and {out_dtype}, expected {[str(t) for t in _FP]}")
-    qp, q_st, q_sh = _heads(q, "q", shape, x_dt, dev)
+        out_dtype = q.dtype if q_out is None else q_out.dtype
     if q_out is None:
-        q_out = torch.empty(shape, dtype=out_dtype, device=q.device)
-    yp, y_st, y_sh = _heads(q_out, "q_out", shape, out_dtype, dev)
-    w = None if q_weight is None else _flat(q_weight, "q_weight", (d,), torch.float32, dev)
-    qs = Heads(qp, yp, w, q_st, q_sh, y_st, y_sh, hq)
-    ks = None
-    if k is not None:
-        k_shape = (n, _dims(k, "k", 3, "[tokens, heads, head_dim]")[1], d)
-        kp, k_st, k_sh = _heads(k, "k", k_shape, x_dt, dev)
-        if k_out is None:
-            k_out = torch.empty(k_shape, dtype=out_dtype, device=q.device)
-        yp, y_st, y_sh = _heads(k_out, "k_out", k_shape, out_dtype, dev)
-        w = None if k_weight is None else _flat(k_weight, "k_weight", (d,), torch.float32, dev)
-        ks = Heads(kp, yp, w, k_st, k_sh, y_st, y_sh, k_shape[1])
-    elif k_out is not None or k_weight is not None:
-        raise ValueError("k_out and k_weight need k")
-    max_pos, half = table = _dims(cos, "cos", 2, "[max_pos, rot_dim / 2]")
-    cp, sp = _flat(cos, "cos", table, torch.float32, dev), _flat(sin, "sin", table, torch.float32, dev)
-    pp = _flat(positions, "positions", (n,), torch.int64, dev)
-    _launch("sherry_qk_norm_rope", (_lib or load()).sherry_qk_norm_rope, _gpu_of(q), qs, ks, _DT[x_dt], _DT[out_dtype], n,
-            d, 2 * half, 1 if interleaved else 0, cp, sp, max_pos, pp, eps)
+        q_out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    elif q_out.dtype != out_dtype:
+        raise ValueError(f"q_out has dtype {q_out.dtype}, expected {out_dtype}")
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=out_dtype, device=k.device)
+    _launch("qk_norm_rope", q.get_device(), q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, q_out, k_out)
     return q_out, k_out
 
 
@@ -693,48 +644,28 @@ class Kv4Cache:
         self.data, self.nbytes, self.device = data, nbytes, data.get_device()
         self.n_pages, self.page_size, self.n_kv_heads, self.head_dim = n_pages, page_size, n_kv_heads, head_dim
         self.desc = Kv4CacheDesc(data.data_ptr(), n_pages, page_size, n_kv_heads, head_dim)
-
-
-def _slots(slots, dev):
-    shape = _dims(slots, "slots", 1, "[n]")
-    return shape[0], _flat(slots, "slots", shape, torch.int64, dev)
+        self.address = ctypes.addressof(self.desc)
 
 
 def kv4_write(cache, k, v, slots):
     """Quantise k, v [n, kv_heads, head_dim] (fp32, fp16 or bf16, any token and
     head strides) into the cache at slots (int64 [n], page * page_size + place,
     all different; one outside the cache is skipped) (sherry_kv4_write)."""
-    dev = cache.device
-    n, sp = _slots(slots, dev)
-    shape = (n, cache.n_kv_heads, cache.head_dim)
-    dt = k.dtype
-    if dt not in _FP:
-        raise ValueError(f"k has dtype {dt}, expected one of {[str(t) for t in _FP]}")
-    kp, k_st, k_sh = _heads(k, "k", shape, dt, dev)
-    vp, v_st, v_sh = _heads(v, "v", shape, dt, dev)
-    _launch("sherry_kv4_write", (_lib or load()).sherry_kv4_write, _gpu_of(k), cache.desc, kp, vp, _DT[dt], n, k_st,
-            k_sh, v_st, v_sh, sp)
+    _launch("kv4_write", cache.device, cache.address, cache.device, k, v, slots)
 
 
 def kv4_read(cache, slots, out_dtype=torch.float16, k_out=None, v_out=None):
     """The values that the cache holds at slots (int64 [n]) as k, v
     [n, kv_heads, head_dim]; slots outside the cache read as zeros
     (sherry_kv4_read)."""
-    dev = cache.device
-    n, sp = _slots(slots, dev)
-    shape = (n, cache.n_kv_heads, cache.head_dim)
     if k_out is not None or v_out is not None:
         out_dtype = (k_out if k_out is not None else v_out).dtype
+    shape = (slots.numel(), cache.n_kv_heads, cache.head_dim)
     if k_out is None:
         k_out = torch.empty(shape, dtype=out_dtype, device=cache.data.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=out_dtype, device=cache.data.device)
-    if out_dtype not in _FP:
-        raise ValueError(f"out_dtype {out_dtype}, expected one of {[str(t) for t in _FP]}")
-    kp, k_st, k_sh = _heads(k_out, "k_out", shape, out_dtype, dev)
-    vp, v_st, v_sh = _heads(v_out, "v_out", shape, out_dtype, dev)
-    _launch("sherry_kv4_read", (_lib or load()).sherry_kv4_read, _gpu_of(slots), cache.desc, kp, vp, _DT[out_dtype], n,
-            k_st, k_sh, v_st, v_sh, sp)
+    _launch("kv4_read", cache.device, cache.address, cache.device, k_out, v_out, slots)
     return k_out, v_out
 
 
@@ -755,33 +686,17 @@ def kv4_attn(cache, q, page_table, kv_lens, cu_q=None, max_q=1, max_kv=None, sca
     the new tokens of a sequence, max_kv (default: what the table holds) sizes
     the launch, scale defaults to head_dim ** -0.5.  A row that sees nothing is
     zeros.  Returns (out, lse fp32 [n, heads] or None)."""
-    dev = cache.device
-    n, hq, d = shape = _dims(q, "q", 3, "[tokens, heads, head_dim]")
-    dt = q.dtype
-    if d != cache.head_dim or dt not in _F16:
-        raise ValueError(f"q has head_dim {d} and dtype {dt}, expected {cache.head_dim} and one of "
-                         f"{[str(t) for t in _F16]}")
-    qp, q_st, q_sh = _heads(q, "q", shape, dt, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=q.device)
-    op, o_st, o_sh = _heads(out, "out", shape, dt, dev)
-    n_seqs, width = t_shape = _dims(page_table, "page_table", 2, "[n_seqs, width]")
-    t_st, t_sd = page_table.stride()
-    if page_table.dtype is not torch.int32 or page_table.get_device() != dev or (t_sd != 1 and width > 1):
-        _refuse(page_table, "page_table", t_shape, torch.int32, dev, "unit-stride (along its rows)")
-    lp = _flat(kv_lens, "kv_lens", (n_seqs,), torch.int32, dev)
-    cp = None if cu_q is None else _flat(cu_q, "cu_q", (n_seqs + 1,), torch.int32, dev)
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if lse is None and want_lse:
-        lse = torch.empty(n, hq, dtype=torch.float32, device=q.device)
-    sp = None if lse is None else _flat(lse, "lse", (n, hq), torch.float32, dev)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     if max_kv is None:
-        max_kv = width * cache.page_size
+        max_kv = page_table.shape[-1] * cache.page_size
     if workspace is None:
-        workspace = kv4_attn_workspace(cache, n, hq, n_seqs, max_q, max_kv)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    if not workspace.is_contiguous() or (workspace.get_device() != dev and ws_bytes):
-        raise ValueError("workspace must be contiguous and on the cache's device")
-    _launch("sherry_kv4_attn", (_lib or load()).sherry_kv4_attn, _gpu_of(q), cache.desc, qp, _DT[dt], n, hq, q_st, q_sh,
-            cp, n_seqs, max_q, max_kv, page_table.data_ptr(), width, t_st, lp, d ** -0.5 if scale is None else scale, op,
-            o_st, o_sh, sp, workspace.data_ptr() or None, ws_bytes)
+        if q.dim() != 3 or page_table.dim() != 2:
+            raise ValueError(f"q must be [tokens, heads, head_dim] and page_table [n_seqs, width], got shapes "
+                             f"{tuple(q.shape)} and {tuple(page_table.shape)}")
+        workspace = kv4_attn_workspace(cache, q.shape[0], q.shape[1], page_table.shape[0], max_q, max_kv)
+    _launch("kv4_attn", cache.device, cache.address, cache.device, q, page_table, kv_lens, cu_q, max_q, max_kv,
+            cache.head_dim ** -0.5 if scale is None else scale, out, lse, workspace)
     return out, lse
