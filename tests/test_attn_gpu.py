@@ -480,6 +480,29 @@ def test_attn_nonfinite_query_stays_in_its_row(gpu_lib):
     assert torch.equal(bad[keep.to(DEV)], good[keep.to(DEV)])
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (16, 1, 64), (6, 2, 128), (12, 1, 128)])
+@pytest.mark.parametrize("ls", [[1, 7, 40], [200, 3000], [20000]])
+def test_attn_fp16_precision(gpu_lib, hq, hkv, d, ls):
+    """fp16 results of up to 16 rows carry little beside their own rounding.  P is
+    held in two fp16 numbers, 2^-22 of each term at most, and sums in fp32:
+    (L / 32 + 64) 2^-24 of the terms' magnitudes, whose sum is at most sqrt(L)
+    times what independent values leave of it.  At L = 20000 that is 141
+    (2^-22 + 2^-14.5) < 0.006, but of errors as often up as down: their root over
+    the L / 32 + 64 additions, 141 * 2^-24 * 26 = 0.0002, is the largest that a
+    sum of random signs reaches, and as a norm it is a quarter of that or less.
+    The rounding's own norm is 0.0002; so 1.25 times it holds with room, where one
+    fp16 number for P gives 1.4."""
+    say("attn fp16 precision", hq, hkv, d, ls)
+    b = Batch(gpu_lib, [1] * len(ls), ls, hq, hkv, d, 32, torch.float16, 1300 + hq)
+    out, _ = b.run()
+    err = own = 0.0
+    for i in range(len(ls)):
+        ref = attn_reference(host(b.q[i:i + 1]).astype(np.float64), b.kd[i], b.vd[i], b.scale, b.dtype)[0]
+        err += ((host(out[i:i + 1]).astype(np.float64) - ref) ** 2).sum()
+        own += ((ref.astype(np.float16).astype(np.float64) - ref) ** 2).sum()
+    assert err <= 1.25 ** 2 * own, (err / own) ** 0.5
+
+
 def test_attn_far_pages(gpu_lib):
     """Pages whose bytes lie past 32-bit offsets."""
     say("attn far pages")

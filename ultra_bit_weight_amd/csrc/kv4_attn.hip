@@ -18,15 +18,23 @@
 //   sum_j p_j v_j = sum_j P_j (c_j - mid) + sum_j p_j (z_j + mid s_j),  P = p s
 // So K enters without rounding, q is brought to fp16 by a power of two (exact
 // for both input types), and the one rounding inside is P to fp16: 2^-11 of
-// each term at most, like the result's own.  mid = 8 centres V's codes: sums of
-// 0..15 would cancel against the zero point's part to a result that over a long
-// axis is hundreds of times smaller (0.0006 instead of 0.0003 of it lost at
-// 131072 tokens).
+// each term at most, like an fp16 result's own, an eighth of a bf16 one's.
+// mid = 7.5 centres V's codes: sums of 0..15 would cancel against the zero
+// point's part to a result that over a long axis is hundreds of times smaller.
 //
-// Unpacking: a code at bits 0-3 of a half is the fp16 subnormal c 2^-24, at
-// bits 4-7 c 2^-20, so for K a mask makes two operands of a dword's eight (the
-// shift by 8 brings the others) and the power of two is taken off the queries;
-// for V a packed addition of -8 follows, and the power of two is taken off O.
+// Of P's rounding error, where results are fp16 and rows few, a second operand
+// is made and multiplied too, which leaves the result's own rounding alone
+// (measured against 64 bits, of the norm: 0.00021, and 0.00031 without it; that
+// costs 3 % of one token over 131072).  With more rows the products are the
+// work, and it would be 30 % of a 2048-token chunk: 0.00031 stays there.
+//
+// Unpacking.  The matrix core aligns a product by its operands' exponent fields
+// and cuts off what falls below, so a subnormal operand with k leading zeros
+// costs k bits of its sums.  V's codes (a mask) are made normal by the fma that
+// centres them.  K's take a shift and a mask, to bits 4-7: 3 to 6 leading zeros
+// keep the scores to 2e-7 of their size (7 to 10 of them, in bits 0-3, to 2e-6; normal
+// numbers, at two instructions more a dword: the same 2e-7, but 7 % of a batch's
+// time).  The powers of two are taken off the scores and off O.
 #include <algorithm>
 #include <type_traits>
 
@@ -48,7 +56,7 @@ constexpr float kPExp = 7.0f;
 constexpr float kPTop = 32768.0f;
 constexpr float kSumTop = 1.0e18f;
 constexpr float kNoMax = -1.0e30f;
-constexpr float kMid = 8.0f;        // centre of V's codes
+constexpr float kMid = 7.5f;        // centre of the codes
 constexpr uint32_t kLoMask = 0x000F000Fu, kHiMask = 0x00F000F0u;
 
 __device__ __forceinline__ half8_t frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -60,15 +68,23 @@ __device__ __forceinline__ f32x4_t mfma(half8_t a, half8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// Two V codes less kMid, in units of 2^-24 (codes in bits 0-3) and 2^-20 (bits
-// 4-7): fp16 subnormals, every step exact.
-__device__ __forceinline__ uint32_t centred_lo(uint32_t w) {
-  constexpr uint32_t kOff = 0x80088008u;  // -8 * 2^-24, twice
-  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, w & kLoMask) + __builtin_bit_cast(half2_t, kOff));
+// V's operands: (code - kMid) 2^-10 from bits 0-3 of each half, 2^-6 from bits
+// 4-7, exact.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t v_pair(uint32_t w) {
+  constexpr _Float16 up = 16384.0f16, off = kHigh ? -kMid / 64 : -kMid / 1024;
+  const half2_t c = __builtin_bit_cast(half2_t, w & (kHigh ? kHiMask : kLoMask));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, half2_t{up, up}, half2_t{off, off}));
 }
-__device__ __forceinline__ uint32_t centred_hi(uint32_t w) {
-  constexpr uint32_t kOff = 0x80808080u;  // -8 * 2^-20, twice
-  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, w & kHiMask) + __builtin_bit_cast(half2_t, kOff));
+template <bool kHigh>
+__device__ __forceinline__ half8_t v_operand(uint32_t w0, uint32_t w1) {
+  return frag(v_pair<kHigh>(w0), v_pair<kHigh>(w0 >> 8), v_pair<kHigh>(w1), v_pair<kHigh>(w1 >> 8));
+}
+// K's operands: codes in bits 4-7, fp16 subnormals of 2^-20.
+template <bool kHigh>
+__device__ __forceinline__ half8_t k_operand(uint32_t w0, uint32_t w1) {
+  if (kHigh) return frag(w0 & kHiMask, (w0 >> 8) & kHiMask, w1 & kHiMask, (w1 >> 8) & kHiMask);
+  return frag((w0 << 4) & kHiMask, (w0 >> 4) & kHiMask, (w1 << 4) & kHiMask, (w1 >> 4) & kHiMask);
 }
 
 // fp16 value i of four packed dwords, as fp32
@@ -118,18 +134,6 @@ __device__ __forceinline__ Place place(const AttnArgs& a) {
   p.seq = i - back * a.n_seqs;
   p.tile = a.row_tiles - 1 - back;
   return p;
-}
-
-// Operands made of a pair of dwords: K (low or high nibbles) and V.
-template <bool kHigh>
-__device__ __forceinline__ half8_t k_operand(uint32_t w0, uint32_t w1) {
-  constexpr uint32_t mask = kHigh ? kHiMask : kLoMask;
-  return frag(w0 & mask, (w0 >> 8) & mask, w1 & mask, (w1 >> 8) & mask);
-}
-template <bool kHigh>
-__device__ __forceinline__ half8_t v_operand(uint32_t w0, uint32_t w1) {
-  if (kHigh) return frag(centred_hi(w0), centred_hi(w0 >> 8), centred_hi(w1), centred_hi(w1 >> 8));
-  return frag(centred_lo(w0), centred_lo(w0 >> 8), centred_lo(w1), centred_lo(w1 >> 8));
 }
 
 // Codes of one block as a lane loads them.
@@ -210,6 +214,7 @@ struct Queries {
     m = fmaxf(m, __shfl_xor(m, 32));
     return m < __builtin_inff() ? m : 0.0f;
   }
+  // sum of each scale group, times unit
   __device__ __forceinline__ void sums(float unit, float (&sumq)[D / 64]) const {
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
@@ -221,13 +226,12 @@ struct Queries {
       sumq[i] = s * unit;
     }
   }
-  // fp16 operands, the row's largest at 2^11, odd products (codes in bits 4-7)
-  // 2^-4 of that
+  // fp16 operands, the row's largest at 2^11
   __device__ __forceinline__ void operands(int e, half8_t (&q)[D / 32]) const {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[i][j] = static_cast<_Float16>(__builtin_ldexpf(f[i][j], 11 - e - 4 * (i & 1)));
+      for (int j = 0; j < 8; ++j) q[i][j] = static_cast<_Float16>(__builtin_ldexpf(f[i][j], 11 - e));
   }
 };
 
@@ -256,7 +260,7 @@ struct Acc {
   }
   // value i of tile nt: odd tiles are made of high nibbles
   __device__ __forceinline__ float value(int nt, int i) const {
-    return __builtin_fmaf(o[nt][i], nt & 1 ? 1048576.0f : 16777216.0f, w[nt >> 2]);
+    return __builtin_fmaf(o[nt][i], nt & 1 ? 64.0f : 1024.0f, w[nt >> 2]);
   }
   // after the last block: sums over the four lane groups of a row
   __device__ __forceinline__ void finish() {
@@ -270,42 +274,45 @@ struct Acc {
   }
 };
 
-// The lane's eight tokens' parameters of group k: K scale (with the score scale
-// in it) and zero point, V scale, and V zero point + kMid V scale.
+// The lane's eight tokens' parameters of group k: K scale and zero point, V scale,
+// and V zero point + kMid V scale.
 template <int D>
 struct RawParams {  // made from fp16 as they are used
   const Params<D>& p;
-  float kc;
-  __device__ __forceinline__ float ks(int k, int i) const { return __builtin_fmaf(half_of(p.ks[k], i), kc, 0.0f); }
+  float unit;  // of the products, sums of q included, in powers of two of the softmax
+  __device__ __forceinline__ float ks(int k, int i) const { return half_of(p.ks[k], i); }
   __device__ __forceinline__ float kz(int k, int i) const { return half_of(p.kz[k], i); }
   __device__ __forceinline__ float vs(int k, int i) const { return half_of(p.vs[k], i); }
-  __device__ __forceinline__ float zc(int k, int i) const {
+  __device__ __forceinline__ float vz(int k, int i) const {
     return __builtin_fmaf(half_of(p.vs[k], i), kMid, half_of(p.vz[k], i));
   }
 };
 template <int D>
-struct LdsParams {  // ready-made, in LDS (at the lane group's eight tokens)
+struct LdsParams {  // ready-made, in LDS (at the lane group's eight tokens), the unit in K's
   const float* at;
   __device__ __forceinline__ float ks(int k, int i) const { return at[(4 * k) * kKv4Block + i]; }
   __device__ __forceinline__ float kz(int k, int i) const { return at[(4 * k + 1) * kKv4Block + i]; }
   __device__ __forceinline__ float vs(int k, int i) const { return at[(4 * k + 2) * kKv4Block + i]; }
-  __device__ __forceinline__ float zc(int k, int i) const { return at[(4 * k + 3) * kKv4Block + i]; }
+  __device__ __forceinline__ float vz(int k, int i) const { return at[(4 * k + 3) * kKv4Block + i]; }
 };
 
 // The softmax step of one tile: scores from the products c (S^T of each scale
 // group) to P operands, one per group.  kEdge: tokens from lim on are not seen
 // (t0 is the lane's first token).
-template <int D, bool kEdge, class P>
+template <int D, bool kEdge, bool kTwo, class P>
 __device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D / 64], const P& pr,
-                                             const float (&sumq)[D / 64], int t0, int lim, half8_t (&pf)[D / 64]) {
+                                             const float (&sumq)[D / 64], int t0, int lim,
+                                             half8_t (&pf)[kTwo ? 2 : 1][D / 64]) {
   constexpr int NG = D / 64;
+  constexpr bool kReady = std::is_same_v<P, LdsParams<D>>;  // the unit is in the parameters
   float p[8], ps[NG][8], top, sum;
   auto score = [&](int i, float m) {
-    float u = __builtin_fmaf(pr.kz(0, i), sumq[0], -m);
+    float u = kReady ? __builtin_fmaf(pr.kz(0, i), sumq[0], -m) : pr.kz(0, i) * sumq[0];
 #pragma unroll
     for (int k = 1; k < NG; ++k) u = __builtin_fmaf(pr.kz(k, i), sumq[k], u);
 #pragma unroll
     for (int k = 0; k < NG; ++k) u = __builtin_fmaf(pr.ks(k, i), c[i >> 2][k][i & 3], u);
+    if constexpr (!kReady) u = __builtin_fmaf(u, pr.unit, -m);
     if constexpr (kEdge) u = t0 + 16 * (i >> 2) + (i & 3) < lim ? u : -__builtin_inff();
     return u;
   };
@@ -345,9 +352,14 @@ __device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D 
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a.w[k] = __builtin_fmaf(p[i], pr.zc(k, i), a.w[k]);
-    pf[k] = frag(pack2<kActF16>(ps[k][0], ps[k][1]), pack2<kActF16>(ps[k][2], ps[k][3]),
-                 pack2<kActF16>(ps[k][4], ps[k][5]), pack2<kActF16>(ps[k][6], ps[k][7]));
+    for (int i = 0; i < 8; ++i) a.w[k] = __builtin_fmaf(p[i], pr.vz(k, i), a.w[k]);
+    pf[0][k] = frag(pack2<kActF16>(ps[k][0], ps[k][1]), pack2<kActF16>(ps[k][2], ps[k][3]),
+                    pack2<kActF16>(ps[k][4], ps[k][5]), pack2<kActF16>(ps[k][6], ps[k][7]));
+    if constexpr (kTwo) {  // (fma again: one mixed-precision instruction)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        pf[1][k][i] = static_cast<_Float16>(__builtin_fmaf(p[i], pr.vs(k, i), -static_cast<float>(pf[0][k][i])));
+    }
   }
 }
 
@@ -390,6 +402,8 @@ template <int D, int DT, int G>
 __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs a) {
   constexpr int NG = D / 64, KS = D / 32, NT = D / 16;
   constexpr int kRows = 16 / G;
+  constexpr bool kTwo = DT == kActF16;  // P's rounding error as a second operand
+  constexpr int kParts = kTwo ? 2 : 1;
   constexpr int kPad = D + 4;  // LDS row stride: 16 rows start 4 banks apart
   __shared__ float lds_o[kAttnWaves][16][kPad];
   __shared__ float lds_m[kAttnWaves][16], lds_l[kAttnWaves][16];
@@ -466,14 +480,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
 
   half8_t q[G][KS];
   float sumq[NG];
-  float kc;
+  float unit;
   {
     Queries<D, DT> f;
     f.load(a.q, (sr.first + tok) * a.q_st + head * a.q_sh + 8 * g);
     const int e = exponent_of(f.top());
-    const float unit = a.scale * kLog2e;
-    f.sums(unit, sumq);
-    kc = __builtin_ldexpf(unit, 24 + e - 11);
+    f.sums(__builtin_ldexpf(1.0f, 11 - e - 20), sumq);  // in the products' unit
+    unit = __builtin_ldexpf(a.scale * kLog2e, 20 + e - 11);
     half8_t t[KS];
     f.operands(e, t);
 #pragma unroll
@@ -512,30 +525,37 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
 #pragma unroll
       for (int b = 0; b < G; ++b) load_k<D>(next.at[b], lane, k[b]);
       const int t0 = (ch * G + copy) * kKv4Block + 4 * g;
-      half8_t pf[NG];
-      if constexpr (edge.value)
-      {
+      half8_t pf[kParts][NG];
+      if constexpr (edge.value) {
         const Params<D> seen = drop_tail<D>(pr, t0, now.mine_there ? sr.len : 0);
-        softmax_step<D, true>(acc, c, RawParams<D>{seen, kc}, sumq, t0, now.mine_there ? lim : 0, pf);
+        softmax_step<D, true, kTwo>(acc, c, RawParams<D>{seen, unit}, sumq, t0, now.mine_there ? lim : 0, pf);
       } else {
-        softmax_step<D, false>(acc, c, RawParams<D>{pr, kc}, sumq, t0, lim, pf);
+        softmax_step<D, false, kTwo>(acc, c, RawParams<D>{pr, unit}, sumq, t0, lim, pf);
       }
       load_p<D>(next.mine, g, pr);
 #pragma unroll
       for (int b = 0; b < G; ++b)
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-          u32x4_t pw = __builtin_bit_cast(u32x4_t, pf[i]);
-          if constexpr (G > 1) {
+          half8_t pb[kParts];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) pw[j] = copy == b ? pw[j] : 0u;
+          for (int h = 0; h < kParts; ++h) {
+            u32x4_t pw = __builtin_bit_cast(u32x4_t, pf[h][i]);
+            if constexpr (G > 1) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) pw[j] = copy == b ? pw[j] : 0u;
+            }
+            pb[h] = __builtin_bit_cast(half8_t, pw);
           }
-          const half8_t pb = __builtin_bit_cast(half8_t, pw);
 #pragma unroll
           for (int j = 2 * i; j < 2 * i + 2; ++j) {
             const u32x2_t w = v[b].pair(j);
-            acc.o[2 * j] = mfma(v_operand<false>(w.x, w.y), pb, acc.o[2 * j]);
-            acc.o[2 * j + 1] = mfma(v_operand<true>(w.x, w.y), pb, acc.o[2 * j + 1]);
+            const half8_t lo = v_operand<false>(w.x, w.y), hi = v_operand<true>(w.x, w.y);
+#pragma unroll
+            for (int h = 0; h < kParts; ++h) {
+              acc.o[2 * j] = mfma(lo, pb[h], acc.o[2 * j]);
+              acc.o[2 * j + 1] = mfma(hi, pb[h], acc.o[2 * j + 1]);
+            }
           }
         }
 #pragma unroll
@@ -702,7 +722,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
     for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, lds_top[w]);
     const int e = exponent_of(top);
     const float unit = a.scale * kLog2e;
-    kc = __builtin_ldexpf(unit, 24 + e - 11);
+    kc = __builtin_ldexpf(unit, 20 + e - 11);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       f[r].sums(unit, sumq[r]);
@@ -742,15 +762,15 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
           }
         }
       const int t0 = b * kKv4Block + 4 * g;
-      half8_t pf[R][NG];
+      half8_t pf[R][1][NG];
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        softmax_step<D, edge.value>(acc[r], c[r], LdsParams<D>{&from.par[0][8 * g]}, sumq[r], t0, lim[r], pf[r]);
+        softmax_step<D, edge.value, false>(acc[r], c[r], LdsParams<D>{&from.par[0][8 * g]}, sumq[r], t0, lim[r], pf[r]);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const half8_t v = __builtin_bit_cast(half8_t, from.v[i][lane]);
 #pragma unroll
-        for (int r = 0; r < R; ++r) acc[r].o[i] = mfma(v, pf[r][i >> 2], acc[r].o[i]);
+        for (int r = 0; r < R; ++r) acc[r].o[i] = mfma(v, pf[r][0][i >> 2], acc[r].o[i]);
       }
     }
     now_there = next_there;
