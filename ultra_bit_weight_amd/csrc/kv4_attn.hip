@@ -389,9 +389,10 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int split, int64_t 
 // copy b are given to block b of the chunk: the products of the G blocks add
 // into one S^T, each with the queries zeroed outside its columns, so one
 // softmax step serves G blocks.  The copies are separate softmaxes, joined with
-// the waves' at the end.  (Rows <= 8: G = 2 against G = 1, same box: 22.4
-// against 23.4 us for one token over 131072, 90 against 104 us for a batch of
-// 48; G = 4 for rows <= 4 costs more registers than it saves: 26 and 107 us.)
+// the waves' at the end.  (Rows <= 8, G = 2 against G = 1: 20.7 against 22.8 us
+// for one token over 131072, 82.7 against 91.3 for a batch of 48; 4.9 against
+// 4.7 for one over 200, where there is little to share.  G = 4 for rows <= 4
+// costs more registers than it saves: 26 and 107 us when G = 2 took 22.4 and 90.)
 //
 // K of the next chunk is loaded as soon as this one's has been multiplied, V
 // and the scales likewise, so loads are in flight during the softmax and the
@@ -609,6 +610,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
 // order of the product's lanes (16-byte accesses without conflicts).  Two
 // buffers: while block b is used, block b + 1 is unpacked behind it and the
 // codes of b + 2 are loaded; one barrier a block.
+//
+// Bound by the vector unit: the softmax is 6 operations and an exponential a
+// score, 83 instructions a lane beside 8 matrix products for a tile of 16 rows x
+// 32 tokens at D = 64.  2048 tokens of 32 heads over 8192, D = 64: 214 us, 560
+// Tflop/s; five ragged prompts, D = 128, bf16: 116 us, 498.  More tiles a wave
+// share the operands' reads: 245 / 244 / 214 us of the chunk with R = 1 / 2 / 4;
+// at D = 128 a third tile does not fit, 140 / 116 us of the prompts with 1 / 2.
 template <int D>
 struct RowsBuf {
   u32x4_t k[2 * D / 32][kWave], v[D / 16][kWave];
@@ -922,10 +930,10 @@ int64_t kv4_attn_tile_rows(int64_t rows, int head_dim) {
 // chip and no more: two workgroups a CU, where that leaves a wave at least 4
 // chunks (few rows) or 8 blocks; and up to 1536 workgroups, for batches of
 // uneven lengths, where it leaves a wave 8 chunks.  Measured, us: one sequence of
-// 131072 tokens, 8 heads of 64: 33.9 / 22.4 / 20.6 / 22.4 / 25.1 with 16 / 32 /
-// 64 / 128 / 192 splits; 48 uneven ones, 8 heads of 128: 101 / 92 / 89 / 95 with
-// 2 / 3 / 4 / 6; a 2048-token chunk over 8192 (256 workgroups): 304 / 232 / 242
-// with 1 / 2 / 4.
+// 131072 tokens, 8 heads of 64: 23.2 / 21.2 / 21.9 / 21.9 with 32 / 64 / 96 / 128
+// splits; 48 uneven ones, 8 heads of 128: 92 / 85 / 82 / 82 / 85 with 2 / 3 / 4 /
+// 5 / 6; a 2048-token chunk over 8192 (256 workgroups): 310 / 214 / 220 with 1 /
+// 2 / 3; ragged prompts that fill the chip by themselves: 116 / 203 with 1 / 2.
 int32_t kv4_attn_splits(int64_t rows, int head_dim, int64_t workgroups, int64_t max_kv) {
   const AttnShape s = attn_shape(rows, head_dim);
   auto share = [&](int64_t want, int64_t unit) {  // unit: tokens of the smallest split
