@@ -480,6 +480,22 @@ def test_attn_nonfinite_query_stays_in_its_row(gpu_lib):
     assert torch.equal(bad[keep.to(DEV)], good[keep.to(DEV)])
 
 
+@pytest.mark.parametrize("qs,ls,bound,hq,hkv,d", [
+    ([130, 3, 64], [130, 200, 64], 200, 4, 1, 64),   # one tile a wave, a chip hardly used
+    ([100, 129], [300, 290], 2100, 40, 10, 64),      # one by its rows, two by its length
+    ([33], [310], 4100, 20, 5, 128),                 # little to share out: one
+    ([140], [300], 4000, 176, 176, 64),              # four: long, and heads that fill the chip
+    ([140], [300], 4000, 176, 176, 128),             # two at most
+    ([65] * 4, [65] * 4, 65, 192, 96, 128)])         # short, but several times the chip
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_attn_tiles_of_rows(gpu_lib, qs, ls, bound, hq, hkv, d, dtype):
+    """Sizes on the several sides of the rule for rows per workgroup (which goes
+    by the bound of the lengths)."""
+    say("attn tiles of rows", qs, ls, bound, hq, hkv, d, dtype)
+    b = Batch(gpu_lib, qs, ls, hq, hkv, d, 64, dtype, 1400 + d)
+    b.check(*b.run(max_kv=bound))
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (16, 1, 64), (6, 2, 128), (12, 1, 128)])
 @pytest.mark.parametrize("ls", [[1, 7, 40], [200, 3000], [20000]])
 def test_attn_fp16_precision(gpu_lib, hq, hkv, d, ls):

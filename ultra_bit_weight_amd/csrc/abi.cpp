@@ -552,11 +552,13 @@ sherry_status attn_sizes(const sherry_kv4_cache* cache, int64_t n_tokens, int32_
   a->group = n_q_heads / a->c.n_kv_heads;
   const int64_t rows = static_cast<int64_t>(max_q) * a->group;
   if (rows > kMaxDim / 256) return SHERRY_ESHAPE;
-  const int64_t tile = kv4_attn_tile_rows(rows, cache->head_dim), tiles = (rows + tile - 1) / tile;
-  if (tiles * n_seqs > kMaxDim / 256 / a->c.n_kv_heads) return SHERRY_ESHAPE;  // threads of the launch
+  const int64_t heads = static_cast<int64_t>(n_seqs) * a->c.n_kv_heads;
+  max_kv = std::min(max_kv, int64_t(1) << 30);
+  a->tile_rows = kv4_attn_tile_rows(rows, heads, cache->head_dim, max_q, max_kv);
+  const int64_t tiles = (rows + a->tile_rows - 1) / a->tile_rows;
+  if (tiles > kMaxDim / 256 / heads) return SHERRY_ESHAPE;  // threads of the launch
   a->row_tiles = static_cast<int32_t>(tiles);
-  a->splits = kv4_attn_splits(rows, cache->head_dim, tiles * n_seqs * a->c.n_kv_heads,
-                              std::min(max_kv, int64_t(1) << 30));
+  a->splits = kv4_attn_splits(a->tile_rows, tiles * heads, max_kv);
   *workspace = a->splits == 1 ? 0 : static_cast<size_t>(a->splits) * n_tokens * n_q_heads * (cache->head_dim + 2) * 4;
   return SHERRY_OK;
 }

@@ -614,9 +614,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
 // Bound by the vector unit: the softmax is 6 operations and an exponential a
 // score, 83 instructions a lane beside 8 matrix products for a tile of 16 rows x
 // 32 tokens at D = 64.  2048 tokens of 32 heads over 8192, D = 64: 214 us, 560
-// Tflop/s; five ragged prompts, D = 128, bf16: 116 us, 498.  More tiles a wave
-// share the operands' reads: 245 / 244 / 214 us of the chunk with R = 1 / 2 / 4;
-// at D = 128 a third tile does not fit, 140 / 116 us of the prompts with 1 / 2.
+// Tflop/s; five ragged prompts, D = 128, bf16: 112 us, 514.
 template <int D>
 struct RowsBuf {
   u32x4_t k[2 * D / 32][kWave], v[D / 16][kWave];
@@ -653,7 +651,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
   const int b_begin = split * per, b_end = min(nblk, b_begin + per);
   const int page_blocks = a.c.page_shift - 5;
   const SHERRY_GLOBAL int32_t* table = gmem(a.table) + static_cast<int64_t>(seq) * a.table_stride;
-  auto block = [&](int b, bool& there) {  // one that is not there reads the cache's first
+  auto block = [&](int at, bool& there) {  // one that is not there reads the cache's first
+    const int b = min(at, b_end - 1);      // (past the last: the last again)
     const int32_t pg = table[b >> page_blocks];
     there = pg >= 0 && pg < a.c.n_pages;
     const int64_t off = kv4_block_off<D>(a.c, there ? pg : 0, kvh, b & ((1 << page_blocks) - 1));
@@ -746,12 +745,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
   for (int r = 0; r < R; ++r) acc[r].clear();
   if (b_begin < b_end) {
     unpack(b_begin, lds[0]);
-    fetch(block(min(b_begin + 1, b_end - 1), next_there));
+    fetch(block(b_begin + 1, next_there));
     __syncthreads();
   }
 
   auto step = [&](int b, auto edge) {
-    const RowsBuf<D>& from = lds[(b - b_begin) & 1];
+    const int turn = b - b_begin;
+    const RowsBuf<D>& from = lds[turn & 1];
     if (now_there && has_rows && (!edge.value || b * kKv4Block < wave_hi)) {
       f32x4_t c[R][2][NG];
 #pragma unroll
@@ -783,8 +783,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
     }
     now_there = next_there;
     if (b + 1 < b_end) {
-      unpack(b + 1, lds[(b + 1 - b_begin) & 1]);
-      fetch(block(min(b + 2, b_end - 1), next_there));
+      unpack(b + 1, lds[(turn + 1) & 1]);
+      fetch(block(b + 2, next_there));
       __syncthreads();
     }
   };
@@ -795,16 +795,16 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     acc[r].finish();
+    float o[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = acc[r].value(i, j);
     const int row = row0 + 16 * r + col;
     if (row >= rows) continue;
     const int tok = a.by_group(row), head = kvh * a.group + (row - tok * a.group);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      float o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = acc[r].value(i, j);
-      store_row<D, DT>(a, split, sr.first + tok, head, 16 * i + 4 * g, o, acc[r].m, acc[r].l);
-    }
+    for (int i = 0; i < NT; ++i) store_row<D, DT>(a, split, sr.first + tok, head, 16 * i + 4 * g, o[i], acc[r].m, acc[r].l);
   }
 }
 
@@ -882,30 +882,14 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(AttnArgs a, int 
   store_row<D, DT>(one, 0, token, hd, 4 * lane, o, m, l);
 }
 
-// How a call is cut up: rows per workgroup (in tiles of 16, `r` a wave, or fewer
-// than 16 in one), and the splits of the cached tokens.
-struct AttnShape {
-  int g;  // blocks per softmax step (rows <= 16 / g), 0: rows kernel
-  int r;  // 16-row tiles per wave of the rows kernel
-};
-
-AttnShape attn_shape(int64_t rows, int head_dim) {
-  if (rows <= 8) return {2, 0};
-  if (rows <= 16) return {1, 0};
-  if (rows <= 16 * kAttnWaves) return {0, 1};
-  if (rows <= 32 * kAttnWaves || head_dim == 128) return {0, 2};
-  return {0, 4};
-}
-
 template <int D, int DT>
 hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.splits) * a.n_seqs * a.row_tiles * a.c.n_kv_heads));
-  const AttnShape s = attn_shape(static_cast<int64_t>(a.max_q) * a.group, D);
   const dim3 block(kAttnThreads);
-  if (s.g == 2) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 2>), grid, block, 0, stream, a);
-  else if (s.g == 1) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 1>), grid, block, 0, stream, a);
-  else if (s.r == 1) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 1>), grid, block, 0, stream, a);
-  else if (s.r == 2) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 2>), grid, block, 0, stream, a);
+  if (a.tile_rows == 8) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 2>), grid, block, 0, stream, a);
+  else if (a.tile_rows == 16) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 1>), grid, block, 0, stream, a);
+  else if (a.tile_rows == 16 * kAttnWaves) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 1>), grid, block, 0, stream, a);
+  else if (a.tile_rows == 32 * kAttnWaves) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 2>), grid, block, 0, stream, a);
   else if constexpr (D == 64) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 4>), grid, block, 0, stream, a);
   if (a.splits > 1) {
     int sg = 0;
@@ -920,9 +904,30 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t kv4_attn_tile_rows(int64_t rows, int head_dim) {
-  const AttnShape s = attn_shape(rows, head_dim);
-  return s.g ? 16 / s.g : 16 * s.r * kAttnWaves;
+// Rows per workgroup.  Up to 8 or 16 rows go to the kernel that shares out the
+// cached tokens.  Beyond, 1, 2 or 4 tiles of 16 rows a wave (2 at most at D =
+// 128, whose registers hold no more): a block's unpacking serves them all, but
+// fewer, longer workgroups fill the chip less evenly, the more so where a
+// prompt's first rows see little.  So one tile for short sequences (mean tokens
+// seen below 1664) while the chip is filled no more than a few times over, and
+// whenever one tile a wave does not fill half of it; four for long ones.  8 key
+// heads, 4 query heads each, us with 1 / 2 / 4 tiles, prompts of q tokens (the
+// last of ctx):
+//   D = 64, q of ctx: 128 of 128  7 / 9 / 13      D = 128: 128 of 128  9 / 12
+//     512 of 512     18 / 21 / 26                   512 of 512     22 / 27
+//     2048 of 2048   47 / 59 / 67                   1024 of 2048   64 / 69
+//     512 of 2048    35 / 32 / 47                   2048 of 4096   216 / 178
+//     4096 of 4096   141 / 117 / 158                4096 of 4096   290 / 237
+//     128 of 4096    27 / 31 / 33                   128 of 4096    39 / 40
+//     2048 of 8192   245 / 244 / 216                512 of 8192    154 / 126
+int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv) {
+  if (rows <= 16) return rows <= 8 ? 8 : 16;
+  constexpr int32_t one = 16 * kAttnWaves;
+  const int64_t tiles = (rows + one - 1) / one * heads;
+  const int64_t seen = std::max(max_kv - max_q / 2, max_q / 2);
+  if (rows <= one || tiles <= 128 || (seen < 1664 && tiles * head_dim < 1536 * 64)) return one;
+  if (head_dim == 128 || rows <= 2 * one || seen < 3328 || tiles < 512) return 2 * one;
+  return 4 * one;
 }
 
 // Splits of the cached tokens.  Each costs a workgroup's start and end (about
@@ -934,14 +939,14 @@ int64_t kv4_attn_tile_rows(int64_t rows, int head_dim) {
 // splits; 48 uneven ones, 8 heads of 128: 92 / 85 / 82 / 82 / 85 with 2 / 3 / 4 /
 // 5 / 6; a 2048-token chunk over 8192 (256 workgroups): 310 / 214 / 220 with 1 /
 // 2 / 3; ragged prompts that fill the chip by themselves: 116 / 203 with 1 / 2.
-int32_t kv4_attn_splits(int64_t rows, int head_dim, int64_t workgroups, int64_t max_kv) {
-  const AttnShape s = attn_shape(rows, head_dim);
+int32_t kv4_attn_splits(int32_t tile_rows, int64_t workgroups, int64_t max_kv) {
+  const bool few = tile_rows <= 16;
   auto share = [&](int64_t want, int64_t unit) {  // unit: tokens of the smallest split
     return std::min((max_kv + unit - 1) / unit, (want + workgroups - 1) / workgroups);
   };
-  const int64_t chunk = s.g ? int64_t(kAttnWaves) * s.g * kKv4Block : kKv4Block;
-  int64_t n = s.g ? share(512, 4 * chunk) : share(512, 8 * chunk);
-  if (s.g) n = std::max(n, share(1536, 8 * chunk));
+  const int64_t chunk = few ? int64_t(kAttnWaves) * (16 / tile_rows) * kKv4Block : kKv4Block;
+  int64_t n = few ? share(512, 4 * chunk) : share(512, 8 * chunk);
+  if (few) n = std::max(n, share(1536, 8 * chunk));
   return static_cast<int32_t>(std::max<int64_t>(1, n));
 }
 

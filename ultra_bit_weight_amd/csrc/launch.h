@@ -319,13 +319,14 @@ struct AttnArgs {
   int32_t group;          // query heads per key head
   int32_t max_q;
   int32_t splits;
+  int32_t tile_rows;      // rows of a workgroup
   int32_t row_tiles;      // workgroups that share the rows, max_q tokens x group
   float scale;
 };
 // Rows (tokens x query heads of one key head) that a workgroup takes, and the
 // shares that a sequence's cached tokens are split into.
-int64_t kv4_attn_tile_rows(int64_t rows, int head_dim);
-int32_t kv4_attn_splits(int64_t rows, int head_dim, int64_t workgroups, int64_t max_kv);
+int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv);
+int32_t kv4_attn_splits(int32_t tile_rows, int64_t workgroups, int64_t max_kv);
 hipError_t launch_kv4_attn(const AttnArgs& a, int head_dim, int dt, hipStream_t stream);
 
 }  // namespace sherry
