@@ -412,7 +412,8 @@ size_t sherry_kv4_attn_workspace(const sherry_kv4_cache* cache /* HOST */, int64
  * of a sequence with L cached tokens sees cached tokens 0 .. L - n + i:
  *   out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
  * A row that sees nothing (L < n - i) gives zeros, and -inf in lse.  Statistics
- * and sums are fp32; the weights and V enter the matrix cores as fp16.
+ * and sums are fp32; the weights enter the matrix cores as fp16, beside the
+ * codes themselves.
  *   q, out     : n_tokens x n_q_heads of dt (F16|BF16); query head h reads key
  *                head h / (n_q_heads / n_kv_heads)
  *   cu_q       : n_seqs + 1 int32, ascending: sequence s has tokens cu_q[s] ..
@@ -424,8 +425,9 @@ size_t sherry_kv4_attn_workspace(const sherry_kv4_cache* cache /* HOST */, int64
  *   max_kv     : the longest sequence's cached tokens, for sizing the launch
  *                only; any value gives the same answer up to rounding
  *   page_table : n_seqs rows of table_width int32 page numbers, row stride
- *                table_stride (0: one row for all); tokens of an entry outside [0, n_pages) are not
- *                seen, entries past a sequence's length not read
+ *                table_stride (0: one row for all); tokens of an entry outside
+ *                [0, n_pages) are not seen, entries past a sequence's length
+ *                not read
  *   kv_lens    : n_seqs int32, L of each (clamped to 0 .. table_width *
  *                page_size, which is at most 2^30)
  *   lse        : n_tokens x n_q_heads fp32, or NULL

@@ -612,9 +612,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
 // codes of b + 2 are loaded; one barrier a block.
 //
 // Bound by the vector unit: the softmax is 6 operations and an exponential a
-// score, 83 instructions a lane beside 8 matrix products for a tile of 16 rows x
-// 32 tokens at D = 64.  2048 tokens of 32 heads over 8192, D = 64: 214 us, 560
-// Tflop/s; five ragged prompts, D = 128, bf16: 112 us, 514.
+// score, 79 instructions a lane beside 8 matrix products for a tile of 16 rows x
+// 32 tokens at D = 64 (vector unit 63 % busy, matrix unit 23 %).  2048 tokens of
+// 32 heads over 8192, D = 64: 212 us with its join (14 us, two splits), 566
+// Tflop/s; five ragged prompts, D = 128, bf16: 112 us, 512.
 template <int D>
 struct RowsBuf {
   u32x4_t k[2 * D / 32][kWave], v[D / 16][kWave];
