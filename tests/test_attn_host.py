@@ -173,3 +173,26 @@ def test_binding_refuses_attn(lib):  # noqa: F811
                 dict(lse=T(3, 8)), dict(workspace=T(100)[::2])):
         with pytest.raises(ValueError):
             sherry.kv4_attn(c, **{**base, **bad})
+
+
+def test_binding_refuses_other_types(lib):  # noqa: F811
+    """Things that are not tensors or numbers, and another count of axes."""
+    c = sherry.Kv4Cache(4, 64, 2, 64, device="cpu")
+    k, slots = T(3, 2, 64), T(3, dtype=torch.int64)
+    for bad in (([1.0], k, slots), (k, None, slots), (k, k, [0, 1, 2])):
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            sherry.kv4_write(c, *bad)
+    q, cs, pos = T(3, 4, 64), T(10, 32, dtype=torch.float32), T(3, dtype=torch.int64)
+    with pytest.raises(TypeError, match="cos must be"):
+        sherry.qk_norm_rope(q, None, None, cs, pos)
+    with pytest.raises(TypeError):
+        sherry.qk_norm_rope(q, None, cs, cs, pos, eps="small")
+    base = dict(q=q, page_table=T(3, 5, dtype=torch.int32), kv_lens=T(3, dtype=torch.int32), workspace=T(0))
+    for bad in (dict(kv_lens=[1, 2, 3]), dict(max_q=1.5), dict(scale="1"), dict(cu_q=(0, 1, 2, 3)), dict(lse=7)):
+        with pytest.raises(TypeError):
+            sherry.kv4_attn(c, **{**base, **bad})
+    for bad in (dict(q=T(3, 256)), dict(page_table=T(15, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="must be"):
+            sherry.kv4_attn(c, **{**base, **bad})
+        with pytest.raises(ValueError, match="must be"):
+            sherry.kv4_attn(c, **{**base, **bad, "workspace": None})
