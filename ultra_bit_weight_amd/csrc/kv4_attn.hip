@@ -931,24 +931,34 @@ int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t ma
   return 4 * one;
 }
 
-// Splits of the cached tokens.  Each costs a workgroup's start and end (about
-// 4 us of latency) and a share of the join, so there are as many as fill the
-// chip and no more: two workgroups a CU, where that leaves a wave at least 4
-// chunks (few rows) or 8 blocks; and up to 1536 workgroups, for batches of
-// uneven lengths, where it leaves a wave 8 chunks.  Measured, us: one sequence of
-// 131072 tokens, 8 heads of 64: 23.2 / 21.2 / 21.9 / 21.9 with 32 / 64 / 96 / 128
-// splits; 48 uneven ones, 8 heads of 128: 92 / 85 / 82 / 82 / 85 with 2 / 3 / 4 /
-// 5 / 6; a 2048-token chunk over 8192 (256 workgroups): 310 / 214 / 220 with 1 /
-// 2 / 3; ragged prompts that fill the chip by themselves: 116 / 203 with 1 / 2.
+// Splits of the cached tokens.  The join costs about 4 us, so nothing is split
+// that a workgroup does in that: 4 steps of its waves (few rows) or 8 blocks.
+// Beyond, one workgroup a CU, down to one step or two blocks each; and where that
+// leaves each enough, for uneven lengths and latency, two a CU (4 steps or 8
+// blocks each) or 1536 workgroups (8 steps), but no number between, which would
+// fill some CUs only (40000 tokens: 13.6 us with 40 splits).
+// Measured, us, 8 key heads, with 1 / 2 / 4 ... splits:
+//   one token, D = 64, over 1000: 7.4 / 8.4 / 8.0 / 8.4
+//     over 4000: 16.7 / 13.0 / 10.4 / 9.3 / 8.6 / 8.5 / 8.7 (64)
+//     over 40000: 124 / 67 / 38 / 23 / 15.6 / 12.0 / 12.4
+//     over 131072: 23.2 / 21.2 / 21.9 with 32 / 64 / 128
+//   9 of 5 tokens over up to 4099, 16 key heads, D = 128: 20.7 / 21.1 / 19.4 /
+//     20.4 / 22.4 with 2 / 3 / 4 / 5 / 6
+//   48 uneven ones, D = 128: 92 / 85 / 82 / 82 / 85 with 2 / 3 / 4 / 5 / 6
+//   20 rows, D = 64, over 1000: 23.7 / 16.7 / 12.2 / 10.2 / 9.3 / 9.0 (32)
+//   64 rows, D = 128, over 4000: 112 / 62 / 36 / 23 / 17.6 / 16.7 / 21.3 (64)
+//   8192 rows over 8192 (256 workgroups): 310 / 214 / 221 (4)
 int32_t kv4_attn_splits(int32_t tile_rows, int64_t workgroups, int64_t max_kv) {
   const bool few = tile_rows <= 16;
-  auto share = [&](int64_t want, int64_t unit) {  // unit: tokens of the smallest split
-    return std::min((max_kv + unit - 1) / unit, (want + workgroups - 1) / workgroups);
-  };
-  const int64_t chunk = few ? int64_t(kAttnWaves) * (16 / tile_rows) * kKv4Block : kKv4Block;
-  int64_t n = few ? share(512, 4 * chunk) : share(512, 8 * chunk);
-  if (few) n = std::max(n, share(1536, 8 * chunk));
-  return static_cast<int32_t>(std::max<int64_t>(1, n));
+  const int64_t step = few ? int64_t(kAttnWaves) * (16 / tile_rows) * kKv4Block : kKv4Block;
+  if (max_kv <= (few ? 4 : 8) * step) return 1;
+  auto splits_to = [&](int64_t total) { return (total + workgroups - 1) / workgroups; };
+  const int64_t least = few ? step : 2 * step;
+  int64_t n = std::min(splits_to(256), (max_kv + least - 1) / least);
+  const int64_t two = splits_to(512), six = splits_to(1536);
+  if (max_kv >= two * (few ? 4 : 8) * step) n = two;
+  if (few && max_kv >= six * 8 * step) n = six;
+  return static_cast<int32_t>(n);
 }
 
 hipError_t launch_kv4_attn(const AttnArgs& a, int head_dim, int dt, hipStream_t stream) {
