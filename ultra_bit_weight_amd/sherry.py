@@ -74,15 +74,17 @@ _bind = None
 _BIND_PATH = os.path.join(_HERE, "lib", "_sherry_bind.so")
 
 
+def _need_built(path):
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is not built; run `python -c 'import __graft_entry__ as g; g.build()'`")
+
+
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
-    """Load libsherry.so (after torch, so it binds to torch's HIP runtime), and
-    the checks of the attention entry points (csrc/bind.cpp) over it."""
-    global _lib, _bind
+    """Load libsherry.so (after torch, so it binds to torch's HIP runtime)."""
+    global _lib
     if _lib is not None:
         return _lib
-    for need in (path, _BIND_PATH):
-        if not os.path.exists(need):
-            raise RuntimeError(f"{need} is not built; run `python -c 'import __graft_entry__ as g; g.build()'`")
+    _need_built(path)
     lib = ctypes.CDLL(path)
     vp, i64, i32, i = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
     sz = ctypes.c_size_t
@@ -155,11 +157,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                     vp, vp, sz, vp]
     lib.sherry_set_prefill_kernel.restype = i
     lib.sherry_set_prefill_kernel.argtypes = [i]
+    _lib = lib
+    return lib
+
+
+def _load_bind():
+    """The checks of the attention entry points (csrc/bind.cpp) over the library."""
+    global _bind
+    _need_built(_BIND_PATH)
     spec = importlib.util.spec_from_file_location("_sherry_bind", _BIND_PATH)
     bind = importlib.util.module_from_spec(spec)
-    bind.attach(os.path.abspath(path))
-    _lib, _bind = lib, bind
-    return lib
+    bind.attach(os.path.abspath(load()._name))
+    _bind = bind
 
 
 def _check(fn: str, status: int) -> None:
@@ -591,7 +600,7 @@ def _launch(fn_name, dev, *args):
     """The call on device `dev` (an index) and its current stream, whichever
     device is current.  csrc/bind.cpp checks the tensors and calls the C ABI."""
     if _bind is None:
-        load()
+        _load_bind()
     f = getattr(_bind, fn_name)
     if dev < 0:  # refused there, after what else is wrong
         status = f(*args, 0)
