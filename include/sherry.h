@@ -424,7 +424,9 @@ size_t sherry_kv4_attn_workspace(const sherry_kv4_cache* cache /* HOST */, int64
  *                only the first max_q rows are computed)
  *   max_kv     : the longest sequence's cached tokens, for sizing the launch
  *                only; any value gives the same answer up to rounding
- *   scale      : finite; |scale * q| below 2^90
+ *   scale      : finite; |scale * q| below 2^90 and |q| below 2^110 (a row past
+ *                that, or with an infinity or a NaN, has no defined result; its
+ *                neighbours keep theirs, and rows that see nothing hold anything)
  *   page_table : n_seqs rows of table_width int32 page numbers, row stride
  *                table_stride (0: one row for all); tokens of an entry outside
  *                [0, n_pages) are not seen, entries past a sequence's length

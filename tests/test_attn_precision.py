@@ -1,0 +1,162 @@
+"""How exact attention over the 4-bit cache is, by bounds that follow each row's
+own sizes (tests/test_attn_gpu.py bounds every row by the largest one).
+
+With codes c, scale s and zero point z of a value, w a row's softmax weights:
+  score   `size` = scale * max over the row's tokens of sum_d |q_d| (15 s + |z|).
+          A query element enters the matrix core as it is or to 2^-36 of the row's
+          largest; of few rows, K's codes enter with up to six leading zeros, whose
+          sums the core cuts by as many bits: 2^-17 of s |q| a term in the worst
+          case, 2^-18.8 as the root mean square of a uniform cut.  64 of them as a random sum: 2^-15.8 s max|q|, where
+          sum |q| 15 s is about 2^8 s max|q| or more.  2^-23.8 of `size`, so
+          2^-20 leaves it a factor of 14 for its tails, D = 128 and other rows.
+  weight  P = p s is rounded to fp16 in the second product: half a step, 2^-11 at
+          mantissa 1, is 2^-11 / sqrt(3) as a root mean square and with mantissas
+          spread evenly over their logarithm (mean of 1 / m^2 over [1, 2): 0.541)
+          0.425 * 2^-11 of each term w s |c - 7.5|.
+  result  rounded once; its own rounding is taken from the exact result.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attn_ref
+from tests.test_attn_gpu import DEV, HALF, Batch, gen, host, make_kv, randn, say
+
+P_RMS = 0.425 * 2.0 ** -11
+SCORE = 2.0 ** -20
+
+
+def parts(x):
+    """value, 15 s + |z| and s |c - 7.5| of what the cache holds of x"""
+    c, s, z = attn_ref.quantise(host(x))
+    g = c.shape[:-1] + (c.shape[-1] // 64, 64)
+    s64 = np.broadcast_to(s.astype(np.float64)[..., None], g)
+    z64 = np.broadcast_to(np.abs(z.astype(np.float64))[..., None], g)
+    return (attn_ref.dequantise(c, s, z), (15 * s64 + z64).reshape(c.shape),
+            (s64 * np.abs(c.reshape(g) - 7.5)).reshape(c.shape))
+
+
+@np.errstate(invalid="ignore")  # (spoiled rows)
+def exact(q, k, v, scale):
+    """out, lse, size [n, hq] and the root mean square of the weights' rounding
+    [n, hq, d], in fp64; k and v from parts()."""
+    n, hq, d = q.shape
+    length, hkv = k[0].shape[:2]
+    out, var = np.zeros((n, hq, d)), np.zeros((n, hq, d))
+    lse, size = np.full((n, hq), -np.inf), np.zeros((n, hq))
+    seen = np.arange(length)[None, :] <= np.arange(n)[:, None] + length - n
+    for h in range(hq if length else 0):
+        kh = h // (hq // hkv)
+        s = np.where(seen, scale * (q[:, h] @ k[0][:, kh].T), -np.inf)
+        size[:, h] = abs(scale) * np.where(seen, np.abs(q[:, h]) @ k[1][:, kh].T, 0).max(-1)
+        live = seen.any(-1)
+        m = np.where(live, s.max(-1), 0)
+        e = np.exp(s - m[:, None])
+        total = np.where(live, e.sum(-1), 1)
+        lse[live, h] = (m + np.log(total))[live]
+        w = e / total[:, None]
+        out[:, h] = w @ v[0][:, kh]
+        var[:, h] = (w * w) @ (v[2][:, kh] ** 2)
+    return out, lse, size, P_RMS * np.sqrt(var)
+
+
+def rounded(x, dtype):
+    return torch.from_numpy(x).to(dtype).double().numpy()
+
+
+def check(q, k, v, scale, out, lse, dtype, keep=None, weight_bits=True):
+    """Norm of the results' error against their own rounding and P's; every
+    log-sum against its row's size.  keep [n, hq]: rows that are looked at."""
+    ref, rl, size, p = exact(q, k, v, scale)
+    keep = np.ones(q.shape[:2], bool) if keep is None else keep
+    empty = np.isneginf(rl)
+    assert not out[empty & keep].any() and np.isneginf(lse[empty & keep]).all()
+    keep = keep & ~empty
+    assert np.isfinite(out[keep]).all() and np.isfinite(lse[keep]).all()
+    lerr = np.abs(lse[keep] - rl[keep]) / (2.0 ** -20 + SCORE * size[keep] + 2.0 ** -22 * np.abs(rl[keep]))
+    err = np.linalg.norm((out - ref)[keep])
+    own = np.hypot(np.linalg.norm((rounded(ref, dtype) - ref)[keep]), weight_bits * np.linalg.norm(p[keep]))
+    say(f"   log-sum {lerr.max():.3f} of its bound, result {err / own:.3f} of its rounding")
+    assert lerr.max() <= 1 and err <= 1.25 * own
+
+
+class Rows(Batch):
+    def check_rows(self, out, lse, keep=None, weight_bits=True):
+        at = 0
+        for i, n in enumerate(self.qs):
+            if n:
+                k, v = ([a for a in x[i]] for x in (self.kp, self.vp))
+                f = slice(at, at + n)
+                check(host(self.q[f]).astype(np.float64), k, v, self.scale, host(out[f]).astype(np.float64),
+                      host(lse[f]).astype(np.float64), self.dtype, None if keep is None else keep[f], weight_bits)
+            at += n
+
+    def __init__(self, lib, qs, ls, hq, hkv, d, page_size, dtype, seed, **kw):
+        super().__init__(lib, qs, ls, hq, hkv, d, page_size, dtype, seed, **kw)
+        self.kp, self.vp = [], []
+        for i, length in enumerate(ls):
+            k, v = make_kv(length, hkv, d, dtype, seed + 10 * i + 1) if length else (torch.zeros(0, hkv, d),) * 2
+            self.kp.append(parts(k))
+            self.vp.append(parts(v))
+
+
+# more than 16 rows a key head, on each tile of the many-row rule (its bound of lengths picks the tile)
+MANY = [([40], [300], 300, 4, 2, 64), ([33, 70], [310, 90], 310, 10, 5, 128),
+        ([100, 129], [300, 290], 2100, 40, 10, 64), ([140], [300], 4000, 176, 176, 64),
+        ([140], [300], 4000, 176, 176, 128)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qs,ls,bound,hq,hkv,d", MANY)
+@pytest.mark.parametrize("power", [14, 28, 36, 60, -30])
+def test_one_row_of_another_size(gpu_lib, qs, ls, bound, hq, hkv, d, power):
+    """One bf16 row 2^power times its neighbours leaves them as exact as ever."""
+    say("attn mixed sizes", qs, ls, bound, hq, hkv, d, power)
+    b = Rows(gpu_lib, qs, ls, hq, hkv, d, 64, torch.bfloat16, 2000 + d)
+    b.q[7, 1] *= 2.0 ** power
+    keep = np.ones(b.q.shape[:2], bool)
+    keep[7, 1] = power < 0  # (the large one's scores are past any bound of use)
+    out, lse = b.run(max_kv=bound)
+    b.check_rows(out, lse, keep)
+
+
+@pytest.mark.gpu
+def test_fp16_rows_of_other_sizes(gpu_lib):
+    """fp16 rows at both ends of the type's range in one tile."""
+    say("attn mixed sizes fp16")
+    b = Rows(gpu_lib, [40], [300], 4, 2, 64, 64, torch.float16, 2100)
+    b.q[3] *= 2.0 ** 13
+    b.q[4] *= 2.0 ** -12
+    keep = np.ones(b.q.shape[:2], bool)
+    keep[3] = False
+    out, lse = b.run()
+    b.check_rows(out, lse, keep)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what", [2.0 ** 50, 2.0 ** 126, float("inf"), float("nan")])
+def test_padding_rows_hold_anything(gpu_lib, d, what):
+    """Rows that see nothing (more new tokens than cached ones) may hold any
+    bits: they give zeros, and their neighbours what they give without them."""
+    say("attn padding rows", d, what)
+    b = Rows(gpu_lib, [50, 50], [20, 37], 4, 2, d, 32, torch.bfloat16, 2200)
+    b.q[:30] = what
+    b.q[50:63] = -what
+    b.check_rows(*b.run())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qs,ls,bound,hq,hkv,d", MANY)
+def test_spoiled_rows_stay_alone(gpu_lib, qs, ls, bound, hq, hkv, d):
+    """NaN, infinity and a size past the contract (|scale q| < 2^90) in single
+    rows of a tile of many."""
+    say("attn spoiled rows", qs, ls, bound, hq, hkv, d)
+    b = Rows(gpu_lib, qs, ls, hq, hkv, d, 64, torch.bfloat16, 2300 + d)
+    keep = np.ones(b.q.shape[:2], bool)
+    for row, head, what in ((5, 0, float("nan")), (6, 1, float("inf")), (9, 0, -float("inf")), (11, 1, 2.0 ** 125)):
+        b.q[row, head, 3] = what
+        keep[row, head] = False
+    out, lse = b.run(max_kv=bound)
+    b.check_rows(out, lse, keep)
+    assert torch.isnan(out[5, 0]).all() and not torch.isfinite(out[6, 1]).all()

@@ -13,12 +13,14 @@
 // product's reduction axis the way the first product leaves them.
 //
 // Scale and zero point stay outside the products, whose operands are the codes
-// themselves (exact in fp16) on one side.  Per 64 values, with codes c:
+// themselves (exact in 16 bits) on one side.  Per 64 values, with codes c:
 //   q . k_j = s_j (q . c_j) + z_j sum(q)
 //   sum_j p_j v_j = sum_j P_j (c_j - mid) + sum_j p_j (z_j + mid s_j),  P = p s
-// So K enters without rounding, q is brought to fp16 by a power of two (exact
-// for both input types), and the one rounding inside is P to fp16: 2^-11 of
-// each term at most, like an fp16 result's own, an eighth of a bf16 one's.
+// So K enters without rounding, and q as it is where rows are many; where they
+// are few it is brought to fp16 by a power of two for each row, which rounds
+// what lies below 2^-25 of the row's largest to 2^-36 of that.  The one rounding
+// inside is P to fp16: 2^-11 of each term (2^-32 of the row's largest P where
+// that is more), like an fp16 result's own, an eighth of a bf16 one's.
 // mid = 7.5 centres V's codes: sums of 0..15 would cancel against the zero
 // point's part to a result that over a long axis is hundreds of times smaller.
 //
@@ -31,10 +33,12 @@
 // Unpacking.  The matrix core aligns a product by its operands' exponent fields
 // and cuts off what falls below, so a subnormal operand with k leading zeros
 // costs k bits of its sums.  V's codes (a mask) are made normal by the fma that
-// centres them.  K's take a shift and a mask, to bits 4-7: 3 to 6 leading zeros
-// keep the scores to 2e-7 of their size (7 to 10 of them, in bits 0-3, to 2e-6; normal
-// numbers, at two instructions more a dword: the same 2e-7, but 7 % of a batch's
-// time).  The powers of two are taken off the scores and off O.
+// centres them.  K's, where rows are few, take a shift and a mask, to bits 4-7: 3
+// to 6 leading zeros keep the scores to 2e-7 of their size (7 to 10 of them, in
+// bits 0-3, to 2e-6; normal numbers by an fma: the same 2e-7, but 7 % of a
+// batch's time).  Where rows are many they are 16 + c, whose four bits lie behind
+// an exponent in fp16 as in bf16 (a shift and one mask-and-or), with 16 s taken
+// off z.  The powers of two are taken off the scores and off O.
 #include <algorithm>
 #include <type_traits>
 
@@ -80,11 +84,35 @@ template <bool kHigh>
 __device__ __forceinline__ half8_t v_operand(uint32_t w0, uint32_t w1) {
   return frag(v_pair<kHigh>(w0), v_pair<kHigh>(w0 >> 8), v_pair<kHigh>(w1), v_pair<kHigh>(w1 >> 8));
 }
-// K's operands: codes in bits 4-7, fp16 subnormals of 2^-20.
+// K's operands of few rows: codes in bits 4-7, fp16 subnormals of 2^-20.
 template <bool kHigh>
 __device__ __forceinline__ half8_t k_operand(uint32_t w0, uint32_t w1) {
   if (kHigh) return frag(w0 & kHiMask, (w0 >> 8) & kHiMask, w1 & kHiMask, (w1 >> 8) & kHiMask);
   return frag((w0 << 4) & kHiMask, (w0 >> 4) & kHiMask, (w1 << 4) & kHiMask, (w1 >> 4) & kHiMask);
+}
+
+// K's operands of many rows: 16 + code, in the queries' own type.  So q enters as
+// it is, and rows of any sizes share a workgroup: fp16 for both types needs powers
+// of two for bf16, and one for each row costs a factor a score (2048 tokens over
+// 8192 221 us against 213, ragged prompts 114.7 against 112.1).
+constexpr float kBase = 16.0f;
+template <int DT, bool kHigh>
+__device__ __forceinline__ u32x4_t k_plus_base(uint32_t w0, uint32_t w1) {
+  constexpr bool kF16 = DT == kActF16;
+  // the code at the mantissa's top, bits 6-9 or 3-6 of a half, behind the exponent of 16
+  constexpr uint32_t mask = kF16 ? 0x03C003C0u : 0x00780078u, base = kF16 ? 0x4C004C00u : 0x41804180u;
+  auto at = [](uint32_t w, int from) {  // the code that starts at bit `from` of a half
+    const int left = (kF16 ? 6 : 3) - from;
+    return ((left >= 0 ? w << (left & 31) : w >> (-left & 31)) & mask) | base;
+  };
+  constexpr int lo = kHigh ? 4 : 0;
+  return u32x4_t{at(w0, lo), at(w0, lo + 8), at(w1, lo), at(w1, lo + 8)};
+}
+template <int DT>
+__device__ __forceinline__ f32x4_t mfma_k(u32x4_t k, u32x4_t q, f32x4_t c) {
+  typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
+  if constexpr (DT == kActF16) return mfma(__builtin_bit_cast(half8_t, k), __builtin_bit_cast(half8_t, q), c);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8_t, k), __builtin_bit_cast(bf8_t, q), c, 0, 0, 0);
 }
 
 // fp16 value i of four packed dwords, as fp32
@@ -202,8 +230,7 @@ struct Queries {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) load8<DT>(q, at + 32 * i, f[i]);
   }
-  // largest magnitude of the row, 0 if that is infinite (the row is spoiled, its
-  // neighbours are not)
+  // largest magnitude of the row, 0 if that is infinite
   __device__ __forceinline__ float top() const {
     float m = 0.0f;
 #pragma unroll
@@ -225,6 +252,11 @@ struct Queries {
       s += __shfl_xor(s, 32);
       sumq[i] = s * unit;
     }
+  }
+  // as they came
+  __device__ __forceinline__ u32x4_t bits(int i) const {
+    return u32x4_t{pack2<DT>(f[i][0], f[i][1]), pack2<DT>(f[i][2], f[i][3]), pack2<DT>(f[i][4], f[i][5]),
+                   pack2<DT>(f[i][6], f[i][7])};
   }
   // fp16 operands, the row's largest at 2^11
   __device__ __forceinline__ void operands(int e, half8_t (&q)[D / 32]) const {
@@ -288,7 +320,7 @@ struct RawParams {  // made from fp16 as they are used
   }
 };
 template <int D>
-struct LdsParams {  // ready-made, in LDS (at the lane group's eight tokens), the unit in K's
+struct LdsParams {  // ready-made, in LDS (at the lane group's eight tokens), the unit in K's scale
   const float* at;
   __device__ __forceinline__ float ks(int k, int i) const { return at[(4 * k) * kKv4Block + i]; }
   __device__ __forceinline__ float kz(int k, int i) const { return at[(4 * k + 1) * kKv4Block + i]; }
@@ -606,7 +638,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
 //
 // Here the products and the softmax are the work, so a block is unpacked once
 // for the workgroup's 64 R rows: each wave makes a quarter of the K and V
-// operands and of the parameters (fp32, the score scale in K's), in LDS in the
+// operands and of the parameters (fp32, the score scale in K's scale), in LDS in the
 // order of the product's lanes (16-byte accesses without conflicts).  Two
 // buffers: while block b is used, block b + 1 is unpacked behind it and the
 // codes of b + 2 are loaded; one barrier a block.
@@ -628,7 +660,6 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
   constexpr int NG = D / 64, KS = D / 32, NT = D / 16;
   constexpr int kRows = 16 * R * kAttnWaves;
   __shared__ RowsBuf<D> lds[2];
-  __shared__ float lds_top[kAttnWaves];
   // the queries of two tiles at D = 128 would not fit the registers of two waves
   constexpr bool kLdsQ = D == 128 && R > 1;
   __shared__ u32x4_t lds_q[kLdsQ ? kAttnWaves : 1][kLdsQ ? R : 1][kLdsQ ? KS : 1][kWave];
@@ -676,16 +707,16 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
     if (does_v) vw = *reinterpret_cast<const SHERRY_GLOBAL u32x2_t*>(blk + v_at);
     if (does_p) {
       p0 = *reinterpret_cast<const SHERRY_GLOBAL uint16_t*>(blk + p_at + kind * 64);
-      p1 = *reinterpret_cast<const SHERRY_GLOBAL uint16_t*>(blk + p_at + 128);  // V's scale
+      p1 = *reinterpret_cast<const SHERRY_GLOBAL uint16_t*>(blk + p_at + (kind >> 1) * 128);  // its scale
     }
   };
-  float kc = 0.0f;
+  const float unit = a.scale * kLog2e;
   auto unpack = [&](int b, RowsBuf<D>& to) {
     if (does_k) {
       // products of K: half block t, group gr -> operands 2 gr (low nibbles) and 2 gr + 1
       const int t = D == 64 ? share : share >> 1, gr = D == 64 ? 0 : share & 1;
-      to.k[t * KS + 2 * gr][lane] = __builtin_bit_cast(u32x4_t, k_operand<false>(kw.x, kw.y));
-      to.k[t * KS + 2 * gr + 1][lane] = __builtin_bit_cast(u32x4_t, k_operand<true>(kw.x, kw.y));
+      to.k[t * KS + 2 * gr][lane] = k_plus_base<DT, false>(kw.x, kw.y);
+      to.k[t * KS + 2 * gr + 1][lane] = k_plus_base<DT, true>(kw.x, kw.y);
     }
     if (does_v) {
       to.v[2 * share][lane] = __builtin_bit_cast(u32x4_t, v_operand<false>(vw.x, vw.y));
@@ -696,49 +727,28 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
       const int tok = b * kKv4Block + 16 * ((idx >> 2) & 1) + 4 * (idx >> 3) + (idx & 3);
       const float x = static_cast<float>(__builtin_bit_cast(_Float16, p0));
       const float s = static_cast<float>(__builtin_bit_cast(_Float16, p1));
-      const float v = kind == 0 ? x * kc : (kind == 3 ? __builtin_fmaf(s, kMid, x) : x);
+      const float v = kind & 1 ? __builtin_fmaf(s, kind == 1 ? -kBase : kMid, x) : (kind == 0 ? x * unit : x);
       to.par[(threadIdx.x >> 7) * 4 + kind][idx] = tok < sr.len ? v : 0.0f;
     }
   };
   bool now_there = false, next_there = false;
   if (b_begin < b_end) fetch(block(b_begin, now_there));
 
-  half8_t q[R][KS];
+  u32x4_t q[R][KS];
   float sumq[R][NG];
   int lim[R];
-  {
-    Queries<D, DT> f[R];
-    float top = 0.0f;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int row = min(row0 + 16 * r + col, rows - 1);
-      const int tok = a.by_group(row), head = kvh * a.group + (row - tok * a.group);
-      lim[r] = sr.len - sr.n + tok + 1;
-      f[r].load(a.q, (sr.first + tok) * a.q_st + head * a.q_sh + 8 * g);
-      top = fmaxf(top, f[r].top());
-    }
-    // one exponent for the workgroup's rows (the score scale is in the shared
-    // parameters): a row 2^-25 times smaller than the largest has scores that
-    // much smaller too
-    top = fmaxf(top, __shfl_xor(top, 1));
-    top = fmaxf(top, __shfl_xor(top, 2));
-    top = fmaxf(top, __shfl_xor(top, 4));
-    top = fmaxf(top, __shfl_xor(top, 8));
-    if (lane == 0) lds_top[wave] = top;
-    __syncthreads();
+  for (int r = 0; r < R; ++r) {
+    const int row = min(row0 + 16 * r + col, rows - 1);
+    const int tok = a.by_group(row), head = kvh * a.group + (row - tok * a.group);
+    lim[r] = sr.len - sr.n + tok + 1;
+    Queries<D, DT> f;
+    f.load(a.q, (sr.first + tok) * a.q_st + head * a.q_sh + 8 * g);
+    f.sums(unit, sumq[r]);
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, lds_top[w]);
-    const int e = exponent_of(top);
-    const float unit = a.scale * kLog2e;
-    kc = __builtin_ldexpf(unit, 20 + e - 11);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      f[r].sums(unit, sumq[r]);
-      f[r].operands(e, q[r]);
-      if constexpr (kLdsQ) {  // (read by the wave that writes them)
-#pragma unroll
-        for (int i = 0; i < KS; ++i) lds_q[wave][r][i][lane] = __builtin_bit_cast(u32x4_t, q[r][i]);
-      }
+    for (int i = 0; i < KS; ++i) {
+      q[r][i] = f.bits(i);
+      if constexpr (kLdsQ) lds_q[wave][r][i][lane] = q[r][i];  // (read by the wave that writes them)
     }
   }
   Acc<D> acc[R];
@@ -759,15 +769,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
       for (int i = 0; i < NG; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          half8_t qi[R];
+          u32x4_t qi[R];
 #pragma unroll
-          for (int r = 0; r < R; ++r)
-            qi[r] = kLdsQ ? __builtin_bit_cast(half8_t, lds_q[wave][r][2 * i + e][lane]) : q[r][2 * i + e];
+          for (int r = 0; r < R; ++r) qi[r] = kLdsQ ? lds_q[wave][r][2 * i + e][lane] : q[r][2 * i + e];
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            const half8_t k = __builtin_bit_cast(half8_t, from.k[t * KS + 2 * i + e][lane]);
+            const u32x4_t k = from.k[t * KS + 2 * i + e][lane];
 #pragma unroll
-            for (int r = 0; r < R; ++r) c[r][t][i] = mfma(k, qi[r], e ? c[r][t][i] : f32x4_t{0, 0, 0, 0});
+            for (int r = 0; r < R; ++r) c[r][t][i] = mfma_k<DT>(k, qi[r], e ? c[r][t][i] : f32x4_t{0, 0, 0, 0});
           }
         }
       const int t0 = b * kKv4Block + 4 * g;
