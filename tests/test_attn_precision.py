@@ -6,9 +6,10 @@ With codes c, scale s and zero point z of a value, w a row's softmax weights:
           A query element enters the matrix core as it is or to 2^-36 of the row's
           largest; of few rows, K's codes enter with up to six leading zeros, whose
           sums the core cuts by as many bits: 2^-17 of s |q| a term in the worst
-          case, 2^-18.8 as the root mean square of a uniform cut.  64 of them as a random sum: 2^-15.8 s max|q|, where
-          sum |q| 15 s is about 2^8 s max|q| or more.  2^-23.8 of `size`, so
-          2^-20 leaves it a factor of 14 for its tails, D = 128 and other rows.
+          case, 2^-18.8 as the root mean square of a uniform cut.  64 of them as a
+          random sum: 2^-15.8 s max|q|, where sum |q| 15 s is about 2^8 s max|q| or
+          more.  2^-23.8 of `size`, so 2^-20 leaves it a factor of 14 for its
+          tails, D = 128 and other rows.
   weight  P = p s is rounded to fp16 in the second product: half a step, 2^-11 at
           mantissa 1, is 2^-11 / sqrt(3) as a root mean square and with mantissas
           spread evenly over their logarithm (mean of 1 / m^2 over [1, 2): 0.541)
@@ -98,6 +99,15 @@ class Rows(Batch):
             k, v = make_kv(length, hkv, d, dtype, seed + 10 * i + 1) if length else (torch.zeros(0, hkv, d),) * 2
             self.kp.append(parts(k))
             self.vp.append(parts(v))
+        self.page_size, self.made = page_size, lambda i: make_kv(ls[i], hkv, d, dtype, seed + 10 * i + 1)
+
+    def write(self, i, change):
+        """Sequence i's keys and values again, as `change` makes them of what they were."""
+        k, v = change(*self.made(i))
+        j = torch.arange(len(k), device=DEV)
+        slots = self.table[i].long()[j // self.page_size] * self.page_size + j % self.page_size
+        self.lib.kv4_write(self.cache, k.to(DEV), v.to(DEV), slots)
+        self.kp[i], self.vp[i] = parts(k), parts(v)
 
 
 # more than 16 rows a key head, on each tile of the many-row rule (its bound of lengths picks the tile)
@@ -160,3 +170,46 @@ def test_spoiled_rows_stay_alone(gpu_lib, qs, ls, bound, hq, hkv, d):
     out, lse = b.run(max_kv=bound)
     b.check_rows(out, lse, keep)
     assert torch.isnan(out[5, 0]).all() and not torch.isfinite(out[6, 1]).all()
+
+
+# the few-row kernel (one token, a few, many splits) and the many-row one
+LARGE = [([1], [200], 200, 4, 1, 64), ([3, 2], [40, 300], 300, 6, 2, 128), ([1, 1], [5000, 40], 5000, 8, 2, 64),
+         ([40], [300], 300, 4, 2, 64), ([33, 70], [310, 90], 310, 10, 5, 128), ([40], [900], 100000, 4, 2, 64)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qs,ls,bound,hq,hkv,d", LARGE)
+@pytest.mark.parametrize("dtype,q_power,k_power", [
+    (torch.bfloat16, 14, 0), (torch.bfloat16, 20, 0), (torch.bfloat16, 25, 0), (torch.bfloat16, 31, 0),
+    (torch.bfloat16, 60, 0), (torch.bfloat16, 60, 10), (torch.float16, 12, 0), (torch.float16, 13, 11)])
+def test_large_scores(gpu_lib, qs, ls, bound, hq, hkv, d, dtype, q_power, k_power):
+    """Scores up to 2^80, where the softmax is one token unless two are closer
+    than fp32 can tell (`size` 2^-20, at both ends of the difference): that
+    token's values to their rounding and P's, else something between the values."""
+    say("attn large scores", qs, ls, bound, hq, hkv, d, dtype, q_power, k_power)
+    b = Rows(gpu_lib, qs, ls, hq, hkv, d, 64, dtype, 2400 + d, q_scale=2.0 ** q_power)
+    for i in range(len(ls)):
+        b.write(i, lambda k, v: ((k.float() * 2.0 ** k_power).to(k.dtype), v))
+    out, lse = b.run(max_kv=bound)
+    at = told = 0
+    for i, n in enumerate(qs):
+        q = host(b.q[at:at + n]).astype(np.float64)
+        got, gl = (host(x[at:at + n]).astype(np.float64) for x in (out, lse))
+        _, rl, size, _ = exact(q, b.kp[i], b.vp[i], b.scale)
+        assert (np.abs(gl - rl) <= 2.0 ** -20 + SCORE * size + 2.0 ** -22 * np.abs(rl)).all()
+        for r in range(n):
+            for h in range(hq):
+                kh = h // (hq // hkv)
+                seen = ls[i] - n + r + 1
+                s = b.scale * (b.kp[i][0][:seen, kh] @ q[r, h])
+                v, pv = b.vp[i][0][:seen, kh], 2.0 ** -11 * b.vp[i][2][:seen, kh].max(0)
+                first, second = np.sort(s)[::-1][:2] if seen > 1 else (s[0], -np.inf)
+                lo, hi = v.min(0), v.max(0)
+                if first - second > 2 * SCORE * size[r, h] + 40:  # (e^-40 of the others is nothing)
+                    told += 1
+                    lo = hi = v[s.argmax()]
+                tol = pv + np.maximum(np.abs(lo), np.abs(hi)) * HALF[dtype] + 2.0 ** -20 * b.vp[i][1][:seen, kh].max(0)
+                assert (got[r, h] >= lo - tol).all() and (got[r, h] <= hi + tol).all(), (r, h)
+        at += n
+    say(f"   {told} of {sum(qs) * hq} rows are one token")
+    assert told

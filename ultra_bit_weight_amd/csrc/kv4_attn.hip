@@ -56,6 +56,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // (fp16 ends at 65504).  P keeps full precision down to 2^-21 of the largest.
 // A V scale of 0 (a constant group, a token never written) hides p from P: it
 // counts as 2^-24 for the maximum, and the sum of p is watched too.
+// What is kept as the maximum m is what is subtracted: kPExp less, rounded.
 constexpr float kPExp = 7.0f;
 constexpr float kPTop = 32768.0f;
 constexpr float kSumTop = 1.0e18f;
@@ -338,13 +339,19 @@ __device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D 
   constexpr int NG = D / 64;
   constexpr bool kReady = std::is_same_v<P, LdsParams<D>>;  // the unit is in the parameters
   float p[8], ps[NG][8], top, sum;
+  // The maximum is taken off the rounded score that it was taken of.  Folded into
+  // the first fma it would round apart from that, by units from scores (or parts
+  // of scores) of 2^24 on, and the largest weight be infinite or 0; the operation
+  // costs 219 us against 213 for 2048 tokens over 8192, 113.4 against 112.1 for
+  // ragged prompts, nothing where rows are few.
   auto score = [&](int i, float m) {
-    float u = kReady ? __builtin_fmaf(pr.kz(0, i), sumq[0], -m) : pr.kz(0, i) * sumq[0];
+    float u = pr.kz(0, i) * sumq[0];
 #pragma unroll
     for (int k = 1; k < NG; ++k) u = __builtin_fmaf(pr.kz(k, i), sumq[k], u);
 #pragma unroll
     for (int k = 0; k < NG; ++k) u = __builtin_fmaf(pr.ks(k, i), c[i >> 2][k][i & 3], u);
-    if constexpr (!kReady) u = __builtin_fmaf(u, pr.unit, -m);
+    if constexpr (!kReady) u *= pr.unit;
+    u -= m;
     if constexpr (kEdge) u = t0 + 16 * (i >> 2) + (i & 3) < lim ? u : -__builtin_inff();
     return u;
   };
@@ -352,7 +359,7 @@ __device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D 
     top = 0.0f, sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(score(i, a.m - kPExp));
+      p[i] = __builtin_amdgcn_exp2f(score(i, a.m));
       sum += p[i];
     }
 #pragma unroll
@@ -375,7 +382,7 @@ __device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D 
     }
     mx = fmaxf(mx, __shfl_xor(mx, 16));
     mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float m_new = fmaxf(a.m, mx);
+    const float m_new = fmaxf(a.m, mx - kPExp);
     a.scale(__builtin_amdgcn_exp2f(a.m - m_new));
     a.m = m_new;
     weights();
@@ -410,7 +417,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int split, int64_t 
     *gmem(reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + token * a.o_st + head * a.o_sh + d)) = out;
     if (a.lse && d == 0)
       gmem(a.lse)[token * a.n_q_heads + head] =
-          l == 0.0f ? -__builtin_inff() : (m - kPExp + __builtin_log2f(l)) * kLn2;
+          l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
   }
 }
 
