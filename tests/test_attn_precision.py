@@ -213,3 +213,16 @@ def test_large_scores(gpu_lib, qs, ls, bound, hq, hkv, d, dtype, q_power, k_powe
         at += n
     say(f"   {told} of {sum(qs) * hq} rows are one token")
     assert told
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qs,ls,bound,hq,hkv,d", LARGE)
+def test_every_score_far_below_zero(gpu_lib, qs, ls, bound, hq, hkv, d):
+    """Scores of -2^106 and less on every token (exact ties among them, of exact
+    keys): no row takes them for nothing seen, in a wave, a share or a join."""
+    say("attn negative scores", qs, ls, bound, hq, hkv, d)
+    b = Rows(gpu_lib, qs, ls, hq, hkv, d, 64, torch.bfloat16, 2500 + d)
+    b.q = torch.full_like(b.q, 2.0 ** 92)
+    for i, length in enumerate(ls):
+        b.write(i, lambda k, v: ((-2000.0 - torch.arange(length) % 40).view(-1, 1, 1).expand(k.shape).half(), v.half()))
+    b.check_rows(*b.run(max_kv=bound))

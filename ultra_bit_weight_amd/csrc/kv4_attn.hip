@@ -60,7 +60,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPExp = 7.0f;
 constexpr float kPTop = 32768.0f;
 constexpr float kSumTop = 1.0e18f;
-constexpr float kNoMax = -1.0e30f;
+constexpr float kNoMax = -3.0e38f;  // below every score
 constexpr float kMid = 7.5f;        // centre of the codes
 constexpr uint32_t kLoMask = 0x000F000Fu, kHiMask = 0x00F000F0u;
 
