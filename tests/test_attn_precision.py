@@ -226,3 +226,17 @@ def test_every_score_far_below_zero(gpu_lib, qs, ls, bound, hq, hkv, d):
     for i, length in enumerate(ls):
         b.write(i, lambda k, v: ((-2000.0 - torch.arange(length) % 40).view(-1, 1, 1).expand(k.shape).half(), v.half()))
     b.check_rows(*b.run(max_kv=bound))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qs,ls", [([5], [9]), ([1, 4, 2], [30, 4, 70]), ([40, 3], [300, 3])])
+def test_ragged_call_without_max_q(gpu_lib, qs, ls):
+    """Every row of every sequence is computed, and rows of none are zeros."""
+    say("attn cu_q without max_q", qs, ls)
+    b = Rows(gpu_lib, qs, ls, 4, 2, 64, 64, torch.float16, 2600)
+    b.q = torch.cat([b.q, b.q[:3]])
+    junk = [torch.full_like(b.q, 7.0, device=DEV) for _ in range(4)]  # (what a fresh buffer would hold)
+    del junk
+    out, lse = b.lib.kv4_attn(b.cache, b.q.to(DEV), b.table, b.lens, cu_q=b.cu, want_lse=True)
+    b.check_rows(out, lse)
+    assert not out[sum(qs):].any() and torch.isneginf(lse[sum(qs):]).all()

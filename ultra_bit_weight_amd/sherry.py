@@ -685,20 +685,27 @@ def kv4_attn_workspace(cache, n_tokens, n_q_heads, n_seqs, max_q=1, max_kv=0):
     return torch.empty(nbytes, dtype=torch.uint8, device=cache.data.device)
 
 
-def kv4_attn(cache, q, page_table, kv_lens, cu_q=None, max_q=1, max_kv=None, scale=None, out=None, lse=None,
+def kv4_attn(cache, q, page_table, kv_lens, cu_q=None, max_q=None, max_kv=None, scale=None, out=None, lse=None,
              want_lse=False, workspace=None):
     """Causal attention of new tokens q [n, heads, head_dim] (fp16 or bf16) over
     the cache (sherry_kv4_attn): sequence s has the tokens cu_q[s] ..
     cu_q[s + 1] - 1 (int32 [n_seqs + 1]; without it max_q tokens each), its
     cached tokens (the new ones included) lie in the pages page_table[s]
     (int32 [n_seqs, width]), and kv_lens[s] (int32) counts them.  max_q bounds
-    the new tokens of a sequence, max_kv (default: what the table holds) sizes
-    the launch, scale defaults to head_dim ** -0.5.  A row that sees nothing is
-    zeros.  Returns (out, lse fp32 [n, heads] or None)."""
+    the new tokens of a sequence (default: 1, with cu_q all of q's; a tight bound
+    makes a smaller launch), max_kv (default: what the table holds) sizes the
+    launch, scale defaults to head_dim ** -0.5.  A row that sees nothing is zeros.
+    Rows of no sequence (with cu_q) are left as they were in an `out` or `lse`
+    given, and are like rows that see nothing in one made here.  Returns (out, lse
+    fp32 [n, heads] or None)."""
+    if max_q is None:
+        max_q = 1 if cu_q is None else max(1, q.shape[0])
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = (torch.empty if cu_q is None else torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
     if lse is None and want_lse:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        if cu_q is not None:
+            lse.fill_(float("-inf"))
     if max_kv is None:
         max_kv = page_table.shape[-1] * cache.page_size
     if workspace is None:
