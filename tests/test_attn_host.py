@@ -196,3 +196,20 @@ def test_binding_refuses_other_types(lib):  # noqa: F811
             sherry.kv4_attn(c, **{**base, **bad})
         with pytest.raises(ValueError, match="must be"):
             sherry.kv4_attn(c, **{**base, **bad, "workspace": None})
+
+
+@pytest.mark.parametrize("hkv,group,d", [(8, 4, 64), (1, 16, 128), (8, 3, 128), (40, 1, 64), (2, 7, 128)])
+def test_default_workspace_serves_default_calls(lib, hkv, group, d):  # noqa: F811
+    """kv4_attn_workspace without max_q and max_kv holds what kv4_attn without
+    them asks for: one token a sequence without cu_q, all tokens with it, and a
+    max_kv of whatever the table holds."""
+    c = sherry.Kv4Cache(4, 64, hkv, d, device="cpu")
+    hq = hkv * group
+    lengths = sorted({*range(1, 40), *(int(1.17 ** i) for i in range(1, 140))})
+    for seqs in (1, 2, 3, 7, 16, 48, 191, 300):
+        for n in {seqs, seqs + 1, 3 * seqs, 40 * seqs}:
+            ws = sherry.kv4_attn_workspace(c, n, hq, seqs).numel()
+            for max_q in {1, n} if n == seqs else {n}:
+                known = sherry.kv4_attn_workspace(c, n, hq, seqs, max_q).numel()
+                needs = [lib.sherry_kv4_attn_workspace(c.desc, n, hq, seqs, max_q, length) for length in lengths]
+                assert max(needs) <= known <= ws, (seqs, n, max_q)
