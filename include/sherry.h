@@ -403,7 +403,12 @@ sherry_status sherry_kv4_read(const sherry_kv4_cache* cache /* HOST */, void* k,
                               int64_t v_stride_head, const int64_t* slots, hipStream_t stream);
 
 /* Workspace bytes of sherry_kv4_attn with these arguments (0: none needed, or
- * arguments that it refuses). */
+ * arguments that it refuses).  It grows with max_kv, but a call of fewer
+ * sequences or tokens can need more than one of many, whose workgroups fill the
+ * chip without splitting the cached tokens: a program of changing batches asks
+ * for each, or holds SHERRY_KV4_ATTN_WORKSPACE_MAX bytes, which serve every call
+ * with n_tokens <= n_seqs * max_q. */
+#define SHERRY_KV4_ATTN_WORKSPACE_MAX ((size_t)66 << 20)
 size_t sherry_kv4_attn_workspace(const sherry_kv4_cache* cache /* HOST */, int64_t n_tokens, int32_t n_q_heads,
                                  int32_t n_seqs, int32_t max_q, int64_t max_kv);
 

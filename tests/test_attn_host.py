@@ -213,3 +213,27 @@ def test_default_workspace_serves_default_calls(lib, hkv, group, d):  # noqa: F8
                 known = sherry.kv4_attn_workspace(c, n, hq, seqs, max_q).numel()
                 needs = [lib.sherry_kv4_attn_workspace(c.desc, n, hq, seqs, max_q, length) for length in lengths]
                 assert max(needs) <= known <= ws, (seqs, n, max_q)
+
+
+def test_workspace_bound(lib):  # noqa: F811
+    """The need is not monotone in the batch (fewer sequences can need more), and
+    SHERRY_KV4_ATTN_WORKSPACE_MAX is above every call's."""
+    import re
+
+    from tests.test_abi_host import HEADER
+
+    most = eval(re.search(r"SHERRY_KV4_ATTN_WORKSPACE_MAX \(\(size_t\)(.*)\)", open(HEADER).read()).group(1))
+    assert most == sherry.KV4_ATTN_WORKSPACE_MAX
+    c = cache()
+    one = [lib.sherry_kv4_attn_workspace(c, n, 32, n, 1, 131072) for n in (48, 191, 192)]
+    assert one[2] == 0 < one[0] < one[1]
+    top = 0
+    for hkv in (1, 2, 5, 8, 16, 63, 128, 511, 513):
+        for group in (1, 3, 4, 8, 16, 33):
+            for d in (64, 128):
+                c = cache(heads=hkv, d=d)
+                for seqs in (1, 2, 5, 8, 31, 63, 65, 191, 511):
+                    for max_q in (1, 2, 5, 16, 17, 33, 65, 100, 128, 129, 256, 257, 512, 513, 1024, 2047, 2048, 2049, 20000):
+                        need = lib.sherry_kv4_attn_workspace(c, seqs * max_q, hkv * group, seqs, max_q, 1 << 30)
+                        top = max(top, need)
+    assert most // 2 < top <= most

@@ -964,6 +964,12 @@ int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t ma
 //   20 rows, D = 64, over 1000: 23.7 / 16.7 / 12.2 / 10.2 / 9.3 / 9.0 (32)
 //   64 rows, D = 128, over 4000: 112 / 62 / 36 / 23 / 17.6 / 16.7 / 21.3 (64)
 //   8192 rows over 8192 (256 workgroups): 310 / 214 / 221 (4)
+// The workspace of any call is bounded by that: with 512 workgroups aimed at, a
+// split call of n < 512 has fewer than 512 + n <= 1023 of them, of up to 256 rows
+// of 64 + 2 floats or 128 of 128 + 2; of few rows fewer than 3072, of 16.
+static_assert(1023 * 256 * (64 + 2) * 4 <= SHERRY_KV4_ATTN_WORKSPACE_MAX &&
+              1023 * 128 * (128 + 2) * 4 <= SHERRY_KV4_ATTN_WORKSPACE_MAX &&
+              3071 * 16 * (128 + 2) * 4 <= SHERRY_KV4_ATTN_WORKSPACE_MAX);
 int32_t kv4_attn_splits(int32_t tile_rows, int64_t workgroups, int64_t max_kv) {
   const bool few = tile_rows <= 16;
   const int64_t step = few ? int64_t(kAttnWaves) * (16 / tile_rows) * kKv4Block : kKv4Block;

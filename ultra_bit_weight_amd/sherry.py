@@ -679,12 +679,15 @@ def kv4_read(cache, slots, out_dtype=torch.float16, k_out=None, v_out=None):
 
 
 _ANY_KV = 1 << 30  # the need grows with max_kv, up to this
+KV4_ATTN_WORKSPACE_MAX = 66 << 20  # bytes that serve every call whose tokens are at most n_seqs * max_q
 
 
 def kv4_attn_workspace(cache, n_tokens, n_q_heads, n_seqs, max_q=None, max_kv=None):
     """A workspace for kv4_attn calls of these sizes (sherry_kv4_attn_workspace);
     calls that may run at the same time need one each.  Without max_q it serves
-    calls without max_q, without max_kv any max_kv."""
+    calls without max_q, without max_kv any max_kv.  A smaller batch can need more
+    than a larger one: a program of changing batches asks for each, or holds
+    KV4_ATTN_WORKSPACE_MAX bytes."""
     nbytes = max(load().sherry_kv4_attn_workspace(cache.desc, n_tokens, n_q_heads, n_seqs, q, _ANY_KV if max_kv is None else max_kv)
                  for q in ((1, n_tokens) if max_q is None else (max_q,)))
     return torch.empty(nbytes, dtype=torch.uint8, device=cache.data.device)
