@@ -237,3 +237,16 @@ def test_workspace_bound(lib):  # noqa: F811
                         need = lib.sherry_kv4_attn_workspace(c, seqs * max_q, hkv * group, seqs, max_q, 1 << 30)
                         top = max(top, need)
     assert most // 2 < top <= most
+
+
+@pytest.mark.parametrize("device", [0, 1, "cuda:0", torch.device("cuda", 0), "cpu", None])
+def test_cache_goes_to_the_device_asked_for(lib, device, monkeypatch):  # noqa: F811
+    """Device 0 by its index is device 0, not the current one."""
+    asked, zeros = [], torch.zeros
+
+    def on_host(*a, **kw):
+        asked.append(kw.pop("device"))
+        return zeros(*a, **kw)
+    monkeypatch.setattr(sherry.torch, "zeros", on_host)
+    sherry.Kv4Cache(4, 64, 2, 64, device=device)
+    assert asked == ["cuda" if device is None else device]
