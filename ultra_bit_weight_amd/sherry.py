@@ -293,7 +293,7 @@ def empty_codes(n: int, k: int, device=None) -> torch.Tensor:
     words = packed_bytes(n, k) // 4
     if words == 0:
         raise ValueError(f"invalid shape n={n} k={k}")
-    return torch.empty(words, dtype=torch.int32, device=device or "cuda")
+    return torch.empty(words, dtype=torch.int32, device="cuda" if device is None else device)
 
 
 def pack(w: torch.Tensor, scale_dtype=torch.float16):
@@ -646,7 +646,7 @@ class Kv4Cache:
         if nbytes == 0:
             raise ValueError(f"no cache of {n_pages} pages of {page_size} tokens, {n_kv_heads} heads of {head_dim}")
         if data is None:
-            data = torch.zeros(nbytes, dtype=torch.uint8, device=device or "cuda")
+            data = torch.zeros(nbytes, dtype=torch.uint8, device="cuda" if device is None else device)
         _need(data, "data", dtypes=(torch.uint8,), min_nbytes=nbytes)
         if not data.is_contiguous():
             raise ValueError("data must be contiguous")
