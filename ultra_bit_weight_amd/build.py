@@ -87,8 +87,10 @@ def build_bind(out: str = BIND) -> str:
 
 
 def build(verbose: bool = False, save_temps: bool = False, defines=(), out: str = LIB) -> str:
-    """Compile every source and link `out` (default: the in-tree library).
-    `defines` (NAME=VALUE strings) override the build-time tunables."""
+    """Compile every source and link `out` (default: the in-tree library, and
+    beside it the binding's checks, whose failure is raised when the library is
+    in place: that needs hipcc alone).  `defines` (NAME=VALUE strings) override
+    the build-time tunables."""
     tag = "_".join(d.replace("=", "") for d in defines)
     objdir = os.path.join(BUILD, tag) if tag else BUILD
     os.makedirs(objdir, exist_ok=True)
@@ -97,8 +99,6 @@ def build(verbose: bool = False, save_temps: bool = False, defines=(), out: str 
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         bind = ex.submit(build_bind) if out == LIB else None
         objs = list(ex.map(lambda s: _compile(s, save_temps, objdir, defines), srcs))
-    if bind:
-        bind.result()
     tmp = out + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -107,6 +107,9 @@ def build(verbose: bool = False, save_temps: bool = False, defines=(), out: str 
     os.replace(tmp, out)
     if verbose:
         print(f"built {out}")
+    if bind and bind.exception():
+        raise RuntimeError(f"{out} is built; {BIND}, which the attention calls of the Python binding need, is not: "
+                           f"{bind.exception()}") from bind.exception()
     return out
 
 
