@@ -9,7 +9,9 @@ With codes c, scale s and zero point z of a value, w a row's softmax weights:
           case, 2^-18.8 as the root mean square of a uniform cut.  64 of them as a
           random sum: 2^-15.8 s max|q|, where sum |q| 15 s is about 2^8 s max|q| or
           more.  2^-23.8 of `size`, so 2^-20 leaves it a factor of 14 for its
-          tails, D = 128 and other rows.
+          tails, D = 128 and other rows; of many log-sums the root mean square may
+          be twice 2^-23.8.  A log-sum's own steps (sums of up to L / 32 + 64
+          tokens, a logarithm, a product) are 2^-22 of 1 + itself likewise.
   weight  P = p s is rounded to fp16 in the second product: half a step, 2^-11 at
           mantissa 1, is 2^-11 / sqrt(3) as a root mean square and with mantissas
           spread evenly over their logarithm (mean of 1 / m^2 over [1, 2): 0.541)
@@ -24,7 +26,7 @@ from oracle import attn_ref
 from tests.test_attn_gpu import DEV, HALF, Batch, gen, host, make_kv, randn, say
 
 P_RMS = 0.425 * 2.0 ** -11
-SCORE = 2.0 ** -20
+SCORE, SCORE_RMS = 2.0 ** -20, 2.0 ** -23.8
 
 
 def parts(x):
@@ -39,11 +41,12 @@ def parts(x):
 
 @np.errstate(invalid="ignore")  # (spoiled rows)
 def exact(q, k, v, scale):
-    """out, lse, size [n, hq] and the root mean square of the weights' rounding
-    [n, hq, d], in fp64; k and v from parts()."""
+    """out, lse, size [n, hq] and what the weights' rounding and the scores' error
+    make of a result as a root mean square [n, hq, d] each, in fp64; k and v from
+    parts()."""
     n, hq, d = q.shape
     length, hkv = k[0].shape[:2]
-    out, var = np.zeros((n, hq, d)), np.zeros((n, hq, d))
+    out, var, svar = (np.zeros((n, hq, d)) for _ in range(3))
     lse, size = np.full((n, hq), -np.inf), np.zeros((n, hq))
     seen = np.arange(length)[None, :] <= np.arange(n)[:, None] + length - n
     for h in range(hq if length else 0):
@@ -57,8 +60,10 @@ def exact(q, k, v, scale):
         lse[live, h] = (m + np.log(total))[live]
         w = e / total[:, None]
         out[:, h] = w @ v[0][:, kh]
-        var[:, h] = (w * w) @ (v[2][:, kh] ** 2)
-    return out, lse, size, P_RMS * np.sqrt(var)
+        w2, o, x = w * w, out[:, h], v[0][:, kh]
+        var[:, h] = w2 @ (v[2][:, kh] ** 2)
+        svar[:, h] = w2 @ (x * x) - 2 * o * (w2 @ x) + o * o * w2.sum(-1, keepdims=True)
+    return out, lse, size, P_RMS * np.sqrt(var), SCORE_RMS * size[..., None] * np.sqrt(np.maximum(svar, 0))
 
 
 def rounded(x, dtype):
@@ -68,17 +73,19 @@ def rounded(x, dtype):
 def check(q, k, v, scale, out, lse, dtype, keep=None, weight_bits=True):
     """Norm of the results' error against their own rounding and P's; every
     log-sum against its row's size.  keep [n, hq]: rows that are looked at."""
-    ref, rl, size, p = exact(q, k, v, scale)
+    ref, rl, size, p, ps = exact(q, k, v, scale)
     keep = np.ones(q.shape[:2], bool) if keep is None else keep
     empty = np.isneginf(rl)
     assert not out[empty & keep].any() and np.isneginf(lse[empty & keep]).all()
     keep = keep & ~empty
     assert np.isfinite(out[keep]).all() and np.isfinite(lse[keep]).all()
-    lerr = np.abs(lse[keep] - rl[keep]) / (2.0 ** -20 + SCORE * size[keep] + 2.0 ** -22 * np.abs(rl[keep]))
+    lerr = np.abs(lse[keep] - rl[keep])
+    lmax = (lerr / (2.0 ** -20 + SCORE * size[keep] + 2.0 ** -22 * np.abs(rl[keep]))).max()
+    lrms = np.sqrt(((lerr / (SCORE_RMS * size[keep] + 2.0 ** -22 * (1 + np.abs(rl[keep])))) ** 2).mean())
     err = np.linalg.norm((out - ref)[keep])
-    own = np.hypot(np.linalg.norm((rounded(ref, dtype) - ref)[keep]), weight_bits * np.linalg.norm(p[keep]))
-    say(f"   log-sum {lerr.max():.3f} of its bound, result {err / own:.3f} of its rounding")
-    assert lerr.max() <= 1 and err <= 1.25 * own
+    own = np.linalg.norm([np.linalg.norm(x[keep]) for x in (rounded(ref, dtype) - ref, weight_bits * p, ps)])
+    say(f"   log-sum {lmax:.3f} of its bound, {lrms:.3f} of its rounding, result {err / own:.3f}")
+    assert lmax <= 1 and lrms <= 2 and err <= 1.25 * own
 
 
 class Rows(Batch):
@@ -108,6 +115,35 @@ class Rows(Batch):
         slots = self.table[i].long()[j // self.page_size] * self.page_size + j % self.page_size
         self.lib.kv4_write(self.cache, k.to(DEV), v.to(DEV), slots)
         self.kp[i], self.vp[i] = parts(k), parts(v)
+
+
+def made(dtype, n=40, length=300, hq=4, hkv=2, d=64, seed=2700, q_scale=1.0, q_noise=0.0, p_bits=11):
+    """Attention in fp64 with P rounded to p_bits and q off by q_noise of itself:
+    what check() is given of it."""
+    k, v = (parts(x) for x in make_kv(length, hkv, d, dtype, seed))
+    q = host((randn(n, hq, d, seed=seed + 5) * q_scale).to(dtype)).astype(np.float64)
+    used = q * (1 + q_noise * np.random.default_rng(seed).uniform(-1, 1, q.shape))
+    out, lse = exact(used, k, v, d ** -0.5)[:2]
+    seen = np.arange(length)[None, :] <= np.arange(n)[:, None] + length - n
+    for h in range(hq):
+        kh = h // (hq // hkv)
+        w = np.where(seen, np.exp(d ** -0.5 * (used[:, h] @ k[0][:, kh].T) - lse[:, [h]]), 0)
+        m, e = np.frexp(w)
+        out[:, h] += (np.ldexp(np.rint(m * 2.0 ** p_bits), e - p_bits) - w) @ (np.sign(v[0][:, kh]) * v[2][:, kh])
+    return q, k, v, d ** -0.5, rounded(out, dtype), lse, dtype
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("kw", [{}, dict(d=128, n=33, hq=10), dict(length=1000), dict(q_scale=30.0)])
+def test_bounds_tell_mistakes(dtype, kw):
+    """The bounds hold for 11 bits of P and exact scores, and neither for 8 bits
+    nor for queries that are 2^-11 off (no GPU: computed here)."""
+    check(*made(dtype, **kw))
+    for mistake in (dict(p_bits=8), dict(q_noise=2.0 ** -11)):
+        if kw.get("q_scale") and "p_bits" in mistake:
+            continue  # (few tokens have the weight, whose rounding is a smaller part)
+        with pytest.raises(AssertionError):
+            check(*made(dtype, **kw, **mistake))
 
 
 # more than 16 rows a key head, on each tile of the many-row rule (its bound of lengths picks the tile)
@@ -195,7 +231,7 @@ def test_large_scores(gpu_lib, qs, ls, bound, hq, hkv, d, dtype, q_power, k_powe
     for i, n in enumerate(qs):
         q = host(b.q[at:at + n]).astype(np.float64)
         got, gl = (host(x[at:at + n]).astype(np.float64) for x in (out, lse))
-        _, rl, size, _ = exact(q, b.kp[i], b.vp[i], b.scale)
+        _, rl, size = exact(q, b.kp[i], b.vp[i], b.scale)[:3]
         assert (np.abs(gl - rl) <= 2.0 ** -20 + SCORE * size + 2.0 ** -22 * np.abs(rl)).all()
         for r in range(n):
             for h in range(hq):
@@ -240,3 +276,40 @@ def test_ragged_call_without_max_q(gpu_lib, qs, ls):
     out, lse = b.lib.kv4_attn(b.cache, b.q.to(DEV), b.table, b.lens, cu_q=b.cu, want_lse=True)
     b.check_rows(out, lse)
     assert not out[sum(qs):].any() and torch.isneginf(lse[sum(qs):]).all()
+
+
+FEW = [([1] * 4, [1, 40, 200, 1031], 1031, 4, 1, 64), ([5, 1, 7], [5, 77, 300], 300, 6, 2, 128),
+       ([1, 1], [9001, 20], 9001, 8, 2, 64), ([4, 4], [4099, 700], 4099, 4, 4, 128)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qs,ls,bound,hq,hkv,d", FEW + MANY + [([500], [4000], 4000, 8, 2, 64)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("q_scale", [1.0, 30.0])
+def test_results_to_their_rounding(gpu_lib, qs, ls, bound, hq, hkv, d, dtype, q_scale):
+    """Results carry their own rounding and P's (of up to 16 fp16 rows their own
+    alone), log-sums fp32's."""
+    say("attn precision", qs, ls, bound, hq, hkv, d, dtype, q_scale)
+    b = Rows(gpu_lib, qs, ls, hq, hkv, d, 64, dtype, 2800 + d, q_scale=q_scale)
+    b.check_rows(*b.run(max_kv=bound), weight_bits=dtype == torch.bfloat16 or max(qs) * hq // hkv > 16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("qs,ls,hq,hkv,d", [([1, 1], [9001, 20], 8, 2, 64), ([3], [4000], 4, 2, 128), ([64], [3000], 4, 1, 64)])
+def test_splits_change_a_rounding_step(gpu_lib, qs, ls, hq, hkv, d, dtype):
+    """Any number of splits gives the same results up to a step of the result's
+    type, and mostly the same bits: P's rounding (its own in every split) moves a
+    value by under 2^-11 of its terms, their sum over L tokens by less."""
+    say("attn splits", qs, ls, hq, hkv, d, dtype)
+    b = Rows(gpu_lib, qs, ls, hq, hkv, d, 64, dtype, 2900 + d)
+    outs = []
+    for max_kv in (0, 600, 1200, max(ls), 1 << 30):
+        o, lse = b.run(max_kv=max_kv)
+        b.check_rows(o, lse, weight_bits=dtype == torch.bfloat16 or max(qs) * hq // hkv > 16)
+        outs.append(host(o).astype(np.float64))
+    one = outs[0]
+    for o in outs[1:]:
+        step = 2 * HALF[dtype] * np.maximum(np.abs(o), np.abs(one))
+        assert (np.abs(o - one) <= step + 2.0 ** -11 * max(x[2].max() for x in b.vp)).all()
+        assert np.linalg.norm(o - one) <= np.linalg.norm(step)
