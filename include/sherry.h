@@ -417,7 +417,8 @@ size_t sherry_kv4_attn_workspace(const sherry_kv4_cache* cache /* HOST */, int64
  * of a sequence with L cached tokens sees cached tokens 0 .. L - n + i:
  *   out = sum_j softmax_j(scale * q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
  * A row that sees nothing (L < n - i) gives zeros, and -inf in lse.  Statistics
- * and sums are fp32; the weights enter the matrix cores as fp16, beside the
+ * and sums are fp32; the weights times V's scale enter the matrix cores as fp16
+ * (2^-11 of each, 2^-32 of the row's largest where that is more), beside the
  * codes themselves.
  *   q, out     : n_tokens x n_q_heads of dt (F16|BF16); query head h reads key
  *                head h / (n_q_heads / n_kv_heads)

@@ -78,6 +78,8 @@ def check(q, k, v, scale, out, lse, dtype, keep=None, weight_bits=True):
     empty = np.isneginf(rl)
     assert not out[empty & keep].any() and np.isneginf(lse[empty & keep]).all()
     keep = keep & ~empty
+    if not keep.any():
+        return
     assert np.isfinite(out[keep]).all() and np.isfinite(lse[keep]).all()
     lerr = np.abs(lse[keep] - rl[keep])
     lmax = (lerr / (2.0 ** -20 + SCORE * size[keep] + 2.0 ** -22 * np.abs(rl[keep]))).max()

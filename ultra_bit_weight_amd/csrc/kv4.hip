@@ -16,7 +16,9 @@
 // 20011 tokens of 8 heads of 64 read back in 10.0 us, 5.3 TB/s, the rate of a
 // large copy; 8192 tokens of 8 heads of 128 written in about 14 us, 3.0 TB/s,
 // where the quantiser's arithmetic (20 instructions a value, of them 6 the exact
-// quotient) is half the time.
+// quotient) is half the time: the vector unit is 43 % busy, and a wave waits for
+// half of its life, since a workgroup's load, arithmetic and store follow one
+// another and the eight of a CU begin together.
 #include "kv4.h"
 
 namespace sherry {

@@ -342,8 +342,9 @@ __device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D 
   // The maximum is taken off the rounded score that it was taken of.  Folded into
   // the first fma it would round apart from that, by units from scores (or parts
   // of scores) of 2^24 on, and the largest weight be infinite or 0; the operation
-  // costs 219 us against 213 for 2048 tokens over 8192, 113.4 against 112.1 for
-  // ragged prompts, nothing where rows are few.
+  // costs 219 us against 213 for 2048 tokens over 8192, 113.1 against 112.0 for
+  // ragged prompts, and where rows are few 1 % at most (12.2 against 12.0 for one
+  // token over 40000; 21.2 and 82.8 for 131072 and a batch as before).
   auto score = [&](int i, float m) {
     float u = pr.kz(0, i) * sumq[0];
 #pragma unroll
@@ -650,11 +651,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
 // buffers: while block b is used, block b + 1 is unpacked behind it and the
 // codes of b + 2 are loaded; one barrier a block.
 //
-// Bound by the vector unit: the softmax is 6 operations and an exponential a
-// score, 79 instructions a lane beside 8 matrix products for a tile of 16 rows x
-// 32 tokens at D = 64 (vector unit 63 % busy, matrix unit 23 %).  2048 tokens of
-// 32 heads over 8192, D = 64: 212 us with its join (14 us, two splits), 566
-// Tflop/s; five ragged prompts, D = 128, bf16: 112 us, 512.
+// Bound by the vector unit: the softmax is 7 operations and an exponential a
+// score, 87 instructions a lane beside 8 matrix products for a tile of 16 rows x
+// 32 tokens at D = 64 (vector unit 67 % busy, matrix unit 23 %).  2048 tokens of
+// 32 heads over 8192, D = 64: 219 us with its join (14 us, two splits), 550
+// Tflop/s; five ragged prompts, D = 128, bf16: 113 us, 510.
 template <int D>
 struct RowsBuf {
   u32x4_t k[2 * D / 32][kWave], v[D / 16][kWave];
@@ -930,13 +931,13 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
 // whenever one tile a wave does not fill half of it; four for long ones.  8 key
 // heads, 4 query heads each, us with 1 / 2 / 4 tiles, prompts of q tokens (the
 // last of ctx):
-//   D = 64, q of ctx: 128 of 128  7 / 9 / 13      D = 128: 128 of 128  9 / 12
-//     512 of 512     18 / 21 / 26                   512 of 512     22 / 27
-//     2048 of 2048   47 / 59 / 67                   1024 of 2048   64 / 69
-//     512 of 2048    35 / 32 / 47                   2048 of 4096   216 / 178
-//     4096 of 4096   141 / 117 / 158                4096 of 4096   290 / 237
-//     128 of 4096    27 / 31 / 33                   128 of 4096    39 / 40
-//     2048 of 8192   245 / 244 / 216                512 of 8192    154 / 126
+//   D = 64, q of ctx: 128 of 128  7 / 9 / 12      D = 128: 128 of 128  9 / 12
+//     512 of 512     19 / 21 / 22                   512 of 512     23 / 27
+//     2048 of 2048   51 / 61 / 67                   1024 of 2048   67 / 70
+//     512 of 2048    36 / 32 / 45                   2048 of 4096   214 / 186
+//     4096 of 4096   149 / 121 / 169                4096 of 4096   248 / 247
+//     128 of 4096    27 / 30 / 33                   128 of 4096    39 / 39
+//     2048 of 8192   254 / 253 / 219                512 of 8192    156 / 130
 int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv) {
   if (rows <= 16) return rows <= 8 ? 8 : 16;
   constexpr int32_t one = 16 * kAttnWaves;
@@ -954,16 +955,16 @@ int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t ma
 // blocks each) or 1536 workgroups (8 steps), but no number between, which would
 // fill some CUs only (40000 tokens: 13.6 us with 40 splits).
 // Measured, us, 8 key heads, with 1 / 2 / 4 ... splits:
-//   one token, D = 64, over 1000: 7.4 / 8.4 / 8.0 / 8.4
-//     over 4000: 16.7 / 13.0 / 10.4 / 9.3 / 8.6 / 8.5 / 8.7 (64)
-//     over 40000: 124 / 67 / 38 / 23 / 15.6 / 12.0 / 12.4
-//     over 131072: 23.2 / 21.2 / 21.9 with 32 / 64 / 128
-//   9 of 5 tokens over up to 4099, 16 key heads, D = 128: 20.7 / 21.1 / 19.4 /
-//     20.4 / 22.4 with 2 / 3 / 4 / 5 / 6
-//   48 uneven ones, D = 128: 92 / 85 / 82 / 82 / 85 with 2 / 3 / 4 / 5 / 6
-//   20 rows, D = 64, over 1000: 23.7 / 16.7 / 12.2 / 10.2 / 9.3 / 9.0 (32)
-//   64 rows, D = 128, over 4000: 112 / 62 / 36 / 23 / 17.6 / 16.7 / 21.3 (64)
-//   8192 rows over 8192 (256 workgroups): 310 / 214 / 221 (4)
+//   one token, D = 64, over 1000: 7.5 / 8.5 / 8.0 / 8.4
+//     over 4000: 17.6 / 13.5 / 10.6 / 9.4 / 8.7 / 8.6 / 8.8 (64)
+//     over 40000: 133 / 72 / 40 / 24 / 16.4 / 12.4 / 12.7
+//     over 131072: 23.5 / 22.0 / 21.7 with 32 / 64 / 128
+//   9 of 5 tokens over up to 4099, 16 key heads, D = 128: 20.9 / 21.5 / 19.5 /
+//     20.5 / 22.5 with 2 / 3 / 4 / 5 / 6
+//   48 uneven ones, D = 128: 92 / 86 / 82 / 82 / 85 with 2 / 3 / 4 / 5 / 6
+//   20 rows, D = 64, over 1000: 24.7 / 17.1 / 12.2 / 10.2 / 9.0 / 8.7 (32)
+//   64 rows, D = 128, over 4000: 115 / 63 / 37 / 24 / 17.3 / 16.4 / 20.9 (64)
+//   8192 rows over 8192 (256 workgroups): 322 / 219 / 224 (4)
 // The workspace of any call is bounded by that: with 512 workgroups aimed at, a
 // split call of n < 512 has fewer than 512 + n <= 1023 of them, of up to 256 rows
 // of 64 + 2 floats or 128 of 128 + 2; of few rows fewer than 3072, of 16.

@@ -285,7 +285,8 @@ struct Kv4Rows {
 };
 hipError_t launch_kv4_rows(const Kv4Geom& g, int head_dim, const Kv4Rows& r, int dt, bool write, hipStream_t stream);
 
-// n / d for 0 <= n < 2^31 by a multiplication: the quotient is
+// n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, Division by
+// Invariant Integers using Multiplication, 1994): the quotient is
 // (hi32(n mul) + n) >> shift with shift = ceil(log2 d) and
 // mul = floor(2^32 (2^shift - d) / d) + 1.
 struct FastDiv {
