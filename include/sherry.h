@@ -125,6 +125,50 @@ sherry_status sherry_decode(const uint32_t* codes, int64_t n, int64_t k, int8_t*
 sherry_status sherry_act_quant(const void* x, sherry_dtype x_dt, int64_t m, int64_t k, int64_t ldx, int8_t* xq,
                                int64_t ldq, float* scales, hipStream_t stream);
 
+/* The residual's addition, an RMS norm and the quantization of sherry_act_quant
+ * in one pass, what stands before a layer's q|k|v and gate|up products:
+ *   h[t, j]  = x[t, j] + residual[t, j]          (x without a residual)
+ *   residual_out[t, j] = h[t, j], rounded to r_dt
+ *   a[t]     = fp32(1 / sqrt(sum_j h[t, j]^2 / k + eps))   (this in fp64)
+ *   y[t, j]  = (h[t, j] a[t]) weight[j]
+ *   scales, xq of y as in sherry_act_quant
+ * Every step outside a[t] is one IEEE fp32 operation, so that codes, scales and
+ * residual are what these lines say, bit for bit (the order of the fp64 sum shows
+ * in a[t] for about one row in 10^7).
+ *   x            : m x k of x_dt (F32|F16|BF16), row stride ldx >= k
+ *   residual     : m x k of r_dt (F32|F16|BF16), row stride ldr, or NULL
+ *   residual_out : m x k of r_dt, row stride ldro; NULL exactly if residual is.
+ *                  It may be residual itself (with ldro = ldr)
+ *   weight       : k fp32
+ *   eps          : finite, not negative
+ *   xq           : out, m x k int8, row stride ldq >= k; scales: out, m fp32
+ * All aligned to their element sizes; rows of 16-byte aligned buffers with k a
+ * multiple of 8 go fastest.  A row with a NaN or an infinity, or a sum past fp32,
+ * has unspecified codes and scale; its neighbours keep theirs.
+ * Errors: EINVAL null pointer, m < 0, k <= 0, eps; EDTYPE; ESHAPE k above 2^30, m
+ * above 2^21 - 1 or a row stride below k; EALIGN. */
+sherry_status sherry_rms_norm_quant(const void* x, sherry_dtype x_dt, int64_t m, int64_t k, int64_t ldx,
+                                    const void* residual, int64_t ldr, void* residual_out, int64_t ldro,
+                                    sherry_dtype r_dt, const float* weight, float eps, int8_t* xq, int64_t ldq,
+                                    float* scales, hipStream_t stream);
+
+/* The gated activation of a feed-forward block and the quantization of
+ * sherry_act_quant in one pass, what stands before its down product:
+ *   y[t, j] = act(gate[t, j]) up[t, j]
+ *   scales, xq of y as in sherry_act_quant
+ * in fp32 (act within a few units in its last place).
+ *   gate, up   : m x k of x_dt (F32|F16|BF16), row strides ldg, ldu >= k (the two
+ *                halves of a gate|up product: up = gate + k, both strides 2 k)
+ *   activation : SHERRY_GATE_SILU, g / (1 + exp(-g)), or SHERRY_GATE_GELU_TANH,
+ *                g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2
+ *   xq, scales : as in sherry_rms_norm_quant
+ * Non-finite rows, alignment and errors as sherry_rms_norm_quant; EINVAL also for
+ * another activation. */
+typedef enum { SHERRY_GATE_SILU = 0, SHERRY_GATE_GELU_TANH = 1 } sherry_gate;
+sherry_status sherry_gated_quant(const void* gate, int64_t ldg, const void* up, int64_t ldu, sherry_dtype x_dt,
+                                 int64_t m, int64_t k, sherry_gate activation, int8_t* xq, int64_t ldq, float* scales,
+                                 hipStream_t stream);
+
 /* Batch-1 product of fp activations: x is quantized per token inside the
  * kernel (the rule of sherry_act_quant, bit for bit), then the int8 product
  * and epilogue of sherry_gemv with that scale -- one launch instead of
@@ -402,6 +446,24 @@ sherry_status sherry_kv4_read(const sherry_kv4_cache* cache /* HOST */, void* k,
                               int64_t k_stride_token, int64_t k_stride_head, int64_t v_stride_token,
                               int64_t v_stride_head, const int64_t* slots, hipStream_t stream);
 
+/* What a layer does between its q|k|v product and its attention, in one launch:
+ * norms and rotation of q and k (sherry_qk_norm_rope), k and v into the cache
+ * (sherry_kv4_write).  The k in between is fp32: cache and q are bit for bit what
+ * the two calls with an F32 k make.
+ *   q     : the queries' side with its output of y_dt, or NULL (y_dt unused)
+ *   k     : the keys' side, heads = n_kv_heads; its y must be NULL
+ *   v     : n tokens x n_kv_heads of x_dt
+ *   slots : as sherry_kv4_write; a token whose slot or position is out of range is
+ *           not written (its rotated q is NaN for a bad position)
+ * head_dim is the cache's; the others as in the two calls, errors too (ESHAPE also
+ * for k->heads other than the cache's, EINVAL for k->y).  q's output must overlap
+ * no input but may be q itself. */
+sherry_status sherry_kv4_append(const sherry_kv4_cache* cache /* HOST */, const sherry_heads* q /* HOST */,
+                                const sherry_heads* k /* HOST */, const void* v, int64_t v_stride_token,
+                                int64_t v_stride_head, sherry_dtype x_dt, sherry_dtype y_dt, int64_t n, int32_t rot_dim,
+                                int32_t interleaved, const float* cos, const float* sin, int64_t max_pos,
+                                const int64_t* positions, float eps, const int64_t* slots, hipStream_t stream);
+
 /* Workspace bytes of sherry_kv4_attn with these arguments (0: none needed, or
  * arguments that it refuses).  It grows with max_kv, but a call of fewer
  * sequences or tokens can need more than one of many, whose workgroups fill the
@@ -454,6 +516,28 @@ sherry_status sherry_kv4_attn(const sherry_kv4_cache* cache /* HOST */, const vo
                               const int32_t* kv_lens, float scale, void* out, int64_t out_stride_token,
                               int64_t out_stride_head, float* lse, void* workspace, size_t workspace_bytes,
                               hipStream_t stream);
+
+/* sherry_kv4_attn with a sliding window and first tokens that stay visible: the
+ * token at position p (its place among its sequence's cached tokens, from 0) sees
+ * token j <= p if j > p - window or j < sinks.
+ *   window : at least 1 (the token itself); one of table_width * page_size or more
+ *            leaves everything visible
+ *   sinks  : at least 0
+ * Everything else as sherry_kv4_attn.  Only blocks of 32 tokens in which some row
+ * sees a token are read: page numbers of pages that no row sees may be anything, so
+ * pages behind the window can be given to other sequences, and what a visible block
+ * holds outside every row's view may be anything too.  The workspace is that of
+ * sherry_kv4_attn_window_workspace with the same window and sinks
+ * (SHERRY_KV4_ATTN_WORKSPACE_MAX serves as there). */
+size_t sherry_kv4_attn_window_workspace(const sherry_kv4_cache* cache /* HOST */, int64_t n_tokens, int32_t n_q_heads,
+                                        int32_t n_seqs, int32_t max_q, int64_t max_kv, int64_t window, int64_t sinks);
+sherry_status sherry_kv4_attn_window(const sherry_kv4_cache* cache /* HOST */, const void* q, sherry_dtype dt,
+                                     int64_t n_tokens, int32_t n_q_heads, int64_t q_stride_token, int64_t q_stride_head,
+                                     const int32_t* cu_q, int32_t n_seqs, int32_t max_q, int64_t max_kv,
+                                     const int32_t* page_table, int32_t table_width, int64_t table_stride,
+                                     const int32_t* kv_lens, float scale, int64_t window, int64_t sinks, void* out,
+                                     int64_t out_stride_token, int64_t out_stride_head, float* lse, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream);
 
 /* ---- 2-bit dense-ternary comparator (Sherry Abstract and Figure 2: the
  * 2-bit aligned packing that keeps alignment by wasting bits) ----

@@ -22,8 +22,8 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libsherry.so")
 BIND = os.path.join(LIBDIR, "_sherry_bind.so")
-SOURCES = ["abi.cpp", "pack.hip", "gemv.hip", "gemm.hip", "gemm_bf16.hip", "gemm_prefill.hip", "gemm_tile32.hip", "act.hip", "rope.hip", "kv4.hip",
-           "kv4_attn.hip", "probes.hip"]
+SOURCES = ["abi.cpp", "pack.hip", "gemv.hip", "gemm.hip", "gemm_bf16.hip", "gemm_prefill.hip", "gemm_tile32.hip", "act.hip", "rowq.hip", "rope.hip",
+           "kv4.hip", "kv4_append.hip", "kv4_attn.hip", "probes.hip"]
 ARCH = "gfx950"
 
 

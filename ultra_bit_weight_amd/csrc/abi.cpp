@@ -540,10 +540,16 @@ sherry_status kv4_rows_impl(const sherry_kv4_cache* cache, const void* k, const 
   return launched(launch_kv4_rows(g, cache->head_dim, r, act_dt(dt), write, stream));
 }
 
+// No row sees more than 2^30 tokens, so that is a window of everything.
+constexpr int64_t kAnyWindow = int64_t(1) << 30;
+struct Window {
+  int64_t tokens = kAnyWindow, sinks = 0;
+};
+
 // Launch sizes of an attention call.
 sherry_status attn_sizes(const sherry_kv4_cache* cache, int64_t n_tokens, int32_t n_q_heads, int32_t n_seqs,
-                         int32_t max_q, int64_t max_kv, AttnArgs* a, size_t* workspace) {
-  if (max_q <= 0 || max_kv < 0 || n_q_heads <= 0) return SHERRY_EINVAL;
+                         int32_t max_q, int64_t max_kv, Window w, AttnArgs* a, size_t* workspace) {
+  if (max_q <= 0 || max_kv < 0 || n_q_heads <= 0 || w.tokens <= 0 || w.sinks < 0) return SHERRY_EINVAL;
   if (n_q_heads % a->c.n_kv_heads != 0 || n_q_heads > 65535 || n_tokens > kMaxDim) return SHERRY_ESHAPE;
   a->n_tokens = n_tokens;
   a->n_q_heads = n_q_heads;
@@ -554,11 +560,14 @@ sherry_status attn_sizes(const sherry_kv4_cache* cache, int64_t n_tokens, int32_
   if (rows > kMaxDim / 256) return SHERRY_ESHAPE;
   const int64_t heads = static_cast<int64_t>(n_seqs) * a->c.n_kv_heads;
   max_kv = std::min(max_kv, int64_t(1) << 30);
-  a->tile_rows = kv4_attn_tile_rows(rows, heads, cache->head_dim, max_q, max_kv);
+  // what a row sees at most, and (below) what the rows of a workgroup do together
+  const int64_t most = std::min(w.tokens, kAnyWindow) + std::min(w.sinks, kAnyWindow);
+  a->tile_rows = kv4_attn_tile_rows(rows, heads, cache->head_dim, max_q, max_kv, most);
   const int64_t tiles = (rows + a->tile_rows - 1) / a->tile_rows;
   if (tiles > kMaxDim / 256 / heads) return SHERRY_ESHAPE;  // threads of the launch
   a->row_tiles = static_cast<int32_t>(tiles);
-  a->splits = kv4_attn_splits(a->tile_rows, tiles * heads, max_kv);
+  const int64_t tile_tokens = std::min<int64_t>(max_q, (a->tile_rows + a->group - 1) / a->group);
+  a->splits = kv4_attn_splits(a->tile_rows, tiles * heads, std::min(max_kv, most + tile_tokens));
   *workspace = a->splits == 1 ? 0 : static_cast<size_t>(a->splits) * n_tokens * n_q_heads * (cache->head_dim + 2) * 4;
   return SHERRY_OK;
 }
@@ -566,15 +575,15 @@ sherry_status attn_sizes(const sherry_kv4_cache* cache, int64_t n_tokens, int32_
 sherry_status kv4_attn_impl(const sherry_kv4_cache* cache, const void* q, dt_t dt, int64_t n_tokens, int32_t n_q_heads,
                             int64_t q_st, int64_t q_sh, const int32_t* cu_q, int32_t n_seqs, int32_t max_q,
                             int64_t max_kv, const int32_t* table, int32_t table_width, int64_t table_stride,
-                            const int32_t* kv_lens, float scale, void* out, int64_t o_st, int64_t o_sh, float* lse,
-                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                            const int32_t* kv_lens, float scale, Window w, void* out, int64_t o_st, int64_t o_sh,
+                            float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (n_tokens < 0 || n_seqs < 0) return SHERRY_EINVAL;
   if (n_tokens == 0 || n_seqs == 0) return SHERRY_OK;
   AttnArgs a{};
   size_t need = 0;
   if (sherry_status s = check_cache(cache, &a.c)) return s;
   if (!q || !table || !kv_lens || !out || table_width <= 0) return SHERRY_EINVAL;
-  if (sherry_status s = attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, max_kv, &a, &need)) return s;
+  if (sherry_status s = attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, max_kv, w, &a, &need)) return s;
   if (dt != SHERRY_F16 && dt != SHERRY_BF16) return SHERRY_EDTYPE;
   const int64_t d = cache->head_dim;
   if (!cu_q && n_tokens != static_cast<int64_t>(n_seqs) * max_q) return SHERRY_ESHAPE;
@@ -606,11 +615,23 @@ sherry_status kv4_attn_impl(const sherry_kv4_cache* cache, const void* q, dt_t d
   a.table_stride = table_stride;
   a.table_width = table_width;
   a.scale = scale;
+  // a window of all that the table holds is none
+  if (w.tokens < static_cast<int64_t>(table_width) * cache->page_size) {
+    a.window = static_cast<int32_t>(w.tokens);
+    a.sinks = static_cast<int32_t>(std::min(w.sinks, kAnyWindow));
+  }
   a.by_kv_heads = FastDiv(static_cast<uint32_t>(a.c.n_kv_heads));
   a.by_splits = FastDiv(static_cast<uint32_t>(a.splits));
   a.by_seqs = FastDiv(static_cast<uint32_t>(a.n_seqs));
   a.by_group = FastDiv(static_cast<uint32_t>(a.group));
   return launched(launch_kv4_attn(a, cache->head_dim, act_dt(dt), stream));
+}
+
+// Rows of k values, each with its scale: sizes that the launch reaches, and a row
+// stride that holds a row and keeps every offset in 64 bits.
+bool quant_rows_fit(int64_t m, int64_t k) { return k <= kMaxDim / 2 && m <= kMaxDim / 1024; }
+bool ld_fits(int64_t m, int64_t k, int64_t ld) {
+  return ld >= k && ld <= kMaxStride && m <= (std::numeric_limits<int64_t>::max() / 8) / ld;
 }
 
 }  // namespace
@@ -892,7 +913,17 @@ size_t sherry_kv4_attn_workspace(const sherry_kv4_cache* cache, int64_t n_tokens
   AttnArgs a{};
   size_t need = 0;
   if (n_tokens <= 0 || n_seqs <= 0 || check_cache(cache, &a.c) != SHERRY_OK) return 0;
-  if (attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, max_kv, &a, &need) != SHERRY_OK) return 0;
+  if (attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, max_kv, Window{}, &a, &need) != SHERRY_OK) return 0;
+  return need;
+}
+
+size_t sherry_kv4_attn_window_workspace(const sherry_kv4_cache* cache, int64_t n_tokens, int32_t n_q_heads,
+                                        int32_t n_seqs, int32_t max_q, int64_t max_kv, int64_t window, int64_t sinks) {
+  AttnArgs a{};
+  size_t need = 0;
+  if (n_tokens <= 0 || n_seqs <= 0 || check_cache(cache, &a.c) != SHERRY_OK) return 0;
+  if (attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, max_kv, Window{window, sinks}, &a, &need) != SHERRY_OK)
+    return 0;
   return need;
 }
 
@@ -903,8 +934,125 @@ sherry_status sherry_kv4_attn(const sherry_kv4_cache* cache, const void* q, sher
                               int64_t out_stride_token, int64_t out_stride_head, float* lse, void* workspace,
                               size_t workspace_bytes, hipStream_t stream) {
   return kv4_attn_impl(cache, q, raw(dt), n_tokens, n_q_heads, q_stride_token, q_stride_head, cu_q, n_seqs, max_q,
-                       max_kv, page_table, table_width, table_stride, kv_lens, scale, out, out_stride_token,
+                       max_kv, page_table, table_width, table_stride, kv_lens, scale, Window{}, out, out_stride_token,
                        out_stride_head, lse, workspace, workspace_bytes, stream);
+}
+
+sherry_status sherry_kv4_attn_window(const sherry_kv4_cache* cache, const void* q, sherry_dtype dt, int64_t n_tokens,
+                                     int32_t n_q_heads, int64_t q_stride_token, int64_t q_stride_head,
+                                     const int32_t* cu_q, int32_t n_seqs, int32_t max_q, int64_t max_kv,
+                                     const int32_t* page_table, int32_t table_width, int64_t table_stride,
+                                     const int32_t* kv_lens, float scale, int64_t window, int64_t sinks, void* out,
+                                     int64_t out_stride_token, int64_t out_stride_head, float* lse, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream) {
+  return kv4_attn_impl(cache, q, raw(dt), n_tokens, n_q_heads, q_stride_token, q_stride_head, cu_q, n_seqs, max_q,
+                       max_kv, page_table, table_width, table_stride, kv_lens, scale, Window{window, sinks}, out,
+                       out_stride_token, out_stride_head, lse, workspace, workspace_bytes, stream);
+}
+
+sherry_status sherry_kv4_append(const sherry_kv4_cache* cache, const sherry_heads* q, const sherry_heads* k,
+                                const void* v, int64_t v_stride_token, int64_t v_stride_head, sherry_dtype x_dt,
+                                sherry_dtype y_dt, int64_t n, int32_t rot_dim, int32_t interleaved, const float* cos,
+                                const float* sin, int64_t max_pos, const int64_t* positions, float eps,
+                                const int64_t* slots, hipStream_t stream) {
+  if (n < 0) return SHERRY_EINVAL;
+  if (n == 0) return SHERRY_OK;
+  Kv4Geom g{};
+  if (sherry_status s = check_cache(cache, &g)) return s;
+  if (!k || !k->x || k->y || !v || !cos || !sin || !positions || !slots || max_pos <= 0 || rot_dim <= 0)
+    return SHERRY_EINVAL;
+  if (act_dt(raw(x_dt)) < 0 || (q && act_dt(raw(y_dt)) < 0)) return SHERRY_EDTYPE;
+  const int64_t heads = g.n_kv_heads, d = cache->head_dim;
+  if (k->heads != heads || rot_dim % 16 != 0 || rot_dim > d || n > kMaxDim || max_pos > (int64_t(1) << 40) ||
+      !strides_fit(n, heads, k->x_stride_token, k->x_stride_head) || !strides_fit(n, heads, v_stride_token, v_stride_head))
+    return SHERRY_ESHAPE;
+  RopeArgs a{};
+  if (q)
+    if (sherry_status s = check_heads(q, raw(x_dt), raw(y_dt), n, d, &a.q)) return s;
+  if (n > kMaxDim / 2 / (d / 8) / (heads + a.q.heads)) return SHERRY_ESHAPE;  // threads of the launch
+  if (!rows_aligned(k->x, raw(x_dt), k->x_stride_token, k->x_stride_head) || (k->w && !aligned(k->w, 16)) ||
+      !rows_aligned(v, raw(x_dt), v_stride_token, v_stride_head) || !aligned(cos, 16) || !aligned(sin, 16) ||
+      !aligned(positions, 8) || !aligned(slots, 8))
+    return SHERRY_EALIGN;
+  if (sherry_status s = check_device()) return s;
+  a.k = RopeHeads{k->x, nullptr, k->w, k->x_stride_token, k->x_stride_head, 0, 0, k->heads};
+  a.cos = cos;
+  a.sin = sin;
+  a.pos = positions;
+  a.n = n;
+  a.max_pos = max_pos;
+  a.d = static_cast<int32_t>(d);
+  a.rot = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.lph_shift = d == 64 ? 2 : 3;
+  a.eps = eps;
+  Kv4Rows r{};
+  r.v = v;
+  r.v_st = v_stride_token;
+  r.v_sh = v_stride_head;
+  r.slots = slots;
+  r.n = n;
+  return launched(launch_kv4_append(g, cache->head_dim, a, r, act_dt(raw(x_dt)), q ? act_dt(raw(y_dt)) : kActF16, stream));
+}
+
+sherry_status sherry_rms_norm_quant(const void* x, sherry_dtype x_dt, int64_t m, int64_t k, int64_t ldx,
+                                    const void* residual, int64_t ldr, void* residual_out, int64_t ldro,
+                                    sherry_dtype r_dt, const float* weight, float eps, int8_t* xq, int64_t ldq,
+                                    float* scales, hipStream_t stream) {
+  if (m < 0 || k <= 0) return SHERRY_EINVAL;
+  if (m == 0) return SHERRY_OK;
+  if (!x || !weight || !xq || !scales || (residual == nullptr) != (residual_out == nullptr)) return SHERRY_EINVAL;
+  if (!(eps >= 0.0f) || eps > std::numeric_limits<float>::max()) return SHERRY_EINVAL;
+  const dt_t xd = raw(x_dt), rd = raw(r_dt);
+  if (act_dt(xd) < 0 || (residual && act_dt(rd) < 0)) return SHERRY_EDTYPE;
+  if (!quant_rows_fit(m, k) || !ld_fits(m, k, ldx) || !ld_fits(m, k, ldq) ||
+      (residual && (!ld_fits(m, k, ldr) || !ld_fits(m, k, ldro))))
+    return SHERRY_ESHAPE;
+  if (!aligned(x, dt_size(xd)) || !aligned(weight, 4) || !aligned(scales, 4) ||
+      (residual && (!aligned(residual, dt_size(rd)) || !aligned(residual_out, dt_size(rd)))))
+    return SHERRY_EALIGN;
+  if (sherry_status s = check_device()) return s;
+  NormQuantArgs a{};
+  a.x = x;
+  a.r = residual;
+  a.r_out = residual_out;
+  a.w = weight;
+  a.q = xq;
+  a.scales = scales;
+  a.m = m;
+  a.k = k;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.ldro = ldro;
+  a.ldq = ldq;
+  a.eps = eps;
+  return launched(launch_rms_norm_quant(a, act_dt(xd), residual ? act_dt(rd) : -1, stream));
+}
+
+sherry_status sherry_gated_quant(const void* gate, int64_t ldg, const void* up, int64_t ldu, sherry_dtype x_dt,
+                                 int64_t m, int64_t k, sherry_gate activation, int8_t* xq, int64_t ldq, float* scales,
+                                 hipStream_t stream) {
+  if (m < 0 || k <= 0) return SHERRY_EINVAL;
+  const dt_t act = raw(activation), xd = raw(x_dt);
+  if (act != SHERRY_GATE_SILU && act != SHERRY_GATE_GELU_TANH) return SHERRY_EINVAL;
+  if (m == 0) return SHERRY_OK;
+  if (!gate || !up || !xq || !scales) return SHERRY_EINVAL;
+  if (act_dt(xd) < 0) return SHERRY_EDTYPE;
+  if (!quant_rows_fit(m, k) || !ld_fits(m, k, ldg) || !ld_fits(m, k, ldu) || !ld_fits(m, k, ldq)) return SHERRY_ESHAPE;
+  if (!aligned(gate, dt_size(xd)) || !aligned(up, dt_size(xd)) || !aligned(scales, 4)) return SHERRY_EALIGN;
+  if (sherry_status s = check_device()) return s;
+  GatedQuantArgs a{};
+  a.gate = gate;
+  a.up = up;
+  a.q = xq;
+  a.scales = scales;
+  a.m = m;
+  a.k = k;
+  a.ldg = ldg;
+  a.ldu = ldu;
+  a.ldq = ldq;
+  a.act = act == SHERRY_GATE_SILU ? kGateSilu : kGateGeluTanh;
+  return launched(launch_gated_quant(a, act_dt(xd), stream));
 }
 
 }  // extern "C"

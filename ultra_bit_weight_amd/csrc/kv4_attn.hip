@@ -2,6 +2,9 @@
 //
 //   o_i = sum_j softmax_j(scale q_i . k_j) v_j,  j <= position of i
 //
+// and, with a window, only j > position - window or j < sinks: the blocks between
+// the sinks and the first row's window are not walked (see Walk).
+//
 // One pass over the cache with a running maximum and sum, on blocks of 32
 // cached tokens and tiles of 16 rows (tokens x query heads of one key head):
 //
@@ -209,14 +212,52 @@ __device__ __forceinline__ void load_p(const uint8_t* blk, int g, Params<D>& p) 
   }
 }
 
-// Zeroes the scales of tokens that lie past `len` (their bytes may be anything,
-// and 0 * NaN is not 0); t0 is the lane's first token.
-template <int D>
-__device__ __forceinline__ Params<D> drop_tail(Params<D> p, int t0, int len) {
+// The blocks of cached tokens that a workgroup walks, numbered without a gap.
+// With a window these are the blocks that hold sinks, then those from the first
+// row's window on; without one, all of them up to the last row's position.
+// `whole` to `whole_end`: blocks of which every row sees all.
+template <bool kWin>
+struct Walk {
+  int n;                 // blocks
+  int whole, whole_end;
+  int head, gap;         // blocks before the gap, and blocks left out
+  int low, sinks;        // no row sees tokens sinks .. low - 1
+  // lim_first, lim_last: tokens below them are seen by the first and the last row
+  __device__ __forceinline__ Walk(const AttnArgs& a, int lim_first, int lim_last, int len) {
+    const int lim_lo = max(lim_first, 0), lim_hi = max(min(lim_last, len), 0);
+    n = (lim_hi + kKv4Block - 1) / kKv4Block;
+    whole = 0, whole_end = min(lim_lo, len) / kKv4Block;
+    head = gap = low = sinks = 0;
+    if constexpr (kWin) {
+      sinks = a.sinks;
+      low = max(lim_lo - a.window, 0);
+      head = (min(sinks, lim_hi) + kKv4Block - 1) / kKv4Block;
+      gap = max(low / kKv4Block - head, 0);
+      const int low_last = max(max(lim_last, 0) - a.window, 0);  // where the last row's window begins
+      whole = low_last <= sinks ? 0 : (low_last + kKv4Block - 1) / kKv4Block - gap;
+      n -= gap;
+      whole_end -= gap;
+    }
+  }
+  __device__ __forceinline__ int block(int b) const {  // its number in the sequence
+    if constexpr (kWin) return b < head ? b : b + gap;
+    return b;
+  }
+  __device__ __forceinline__ bool seen(int t, int len) const {  // by any row, as far as its place in the walk says
+    if constexpr (kWin) return t < len && (t >= low || t < sinks);
+    return t < len;
+  }
+};
+
+// Zeroes the scales of tokens that no row sees (their bytes may be anything, and
+// 0 * NaN is not 0): those past `len`, and with a window those before it that are
+// no sinks; t0 is the lane's first token.
+template <int D, bool kWin>
+__device__ __forceinline__ Params<D> drop_unseen(Params<D> p, const Walk<kWin>& walk, int t0, int len) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = t0 + 16 * (i >> 1) + 2 * (i & 1);
-    const uint32_t mask = (t < len ? 0xFFFFu : 0u) | (t + 1 < len ? 0xFFFF0000u : 0u);
+    const uint32_t mask = (walk.seen(t, len) ? 0xFFFFu : 0u) | (walk.seen(t + 1, len) ? 0xFFFF0000u : 0u);
 #pragma unroll
     for (int k = 0; k < D / 64; ++k) p.ks[k][i] &= mask, p.kz[k][i] &= mask, p.vs[k][i] &= mask, p.vz[k][i] &= mask;
   }
@@ -329,12 +370,26 @@ struct LdsParams {  // ready-made, in LDS (at the lane group's eight tokens), th
   __device__ __forceinline__ float vz(int k, int i) const { return at[(4 * k + 3) * kKv4Block + i]; }
 };
 
+// What a row sees: tokens below lim, with a window only from low on or below sinks.
+template <bool kWin>
+struct Sees {
+  int lim, low, sinks;
+  __device__ __forceinline__ bool operator()(int t) const {
+    if constexpr (kWin) return t < lim && (t >= low || t < sinks);
+    return t < lim;
+  }
+};
+template <bool kWin>
+__device__ __forceinline__ Sees<kWin> sees_of(const AttnArgs& a, int lim) {
+  return {lim, max(lim, 0) - a.window, a.sinks};  // (not used without a window)
+}
+
 // The softmax step of one tile: scores from the products c (S^T of each scale
-// group) to P operands, one per group.  kEdge: tokens from lim on are not seen
-// (t0 is the lane's first token).
-template <int D, bool kEdge, bool kTwo, class P>
+// group) to P operands, one per group.  kEdge: not every token is seen (t0 is the
+// lane's first one).
+template <int D, bool kEdge, bool kTwo, bool kWin, class P>
 __device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D / 64], const P& pr,
-                                             const float (&sumq)[D / 64], int t0, int lim,
+                                             const float (&sumq)[D / 64], int t0, const Sees<kWin>& sees,
                                              half8_t (&pf)[kTwo ? 2 : 1][D / 64]) {
   constexpr int NG = D / 64;
   constexpr bool kReady = std::is_same_v<P, LdsParams<D>>;  // the unit is in the parameters
@@ -353,7 +408,7 @@ __device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D 
     for (int k = 0; k < NG; ++k) u = __builtin_fmaf(pr.ks(k, i), c[i >> 2][k][i & 3], u);
     if constexpr (!kReady) u *= pr.unit;
     u -= m;
-    if constexpr (kEdge) u = t0 + 16 * (i >> 2) + (i & 3) < lim ? u : -__builtin_inff();
+    if constexpr (kEdge) u = sees(t0 + 16 * (i >> 2) + (i & 3)) ? u : -__builtin_inff();
     return u;
   };
   auto weights = [&]() {
@@ -439,7 +494,7 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int split, int64_t 
 // other product; the page numbers are read a chunk ahead of that.  After the
 // last chunk the loads repeat it (from L2): a branch around them would make the
 // compiler wait for them where it joins.
-template <int D, int DT, int G>
+template <int D, int DT, int G, bool kWin>
 __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs a) {
   constexpr int NG = D / 64, KS = D / 32, NT = D / 16;
   constexpr int kRows = 16 / G;
@@ -461,15 +516,13 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
   if (row0 >= rows) return;
   const int nrow = min(kRows, rows - row0);
 
-  // row r sees tokens below lim(r)
-  const int lim_lo = max(sr.len - sr.n + a.by_group(row0) + 1, 0);
-  const int lim_hi = max(min(sr.len - sr.n + a.by_group(row0 + nrow - 1) + 1, sr.len), 0);
+  const Walk<kWin> walk(a, sr.len - sr.n + a.by_group(row0) + 1, sr.len - sr.n + a.by_group(row0 + nrow - 1) + 1, sr.len);
   const int row = min(row0 + col % kRows, rows - 1);
   const int tok = a.by_group(row);
   const int head = kvh * a.group + (row - tok * a.group);
-  const int lim = sr.len - sr.n + tok + 1;
+  const Sees<kWin> sees = sees_of<kWin>(a, sr.len - sr.n + tok + 1);
 
-  const int nblk = (lim_hi + kKv4Block - 1) / kKv4Block;
+  const int nblk = walk.n;
   const int chunks = (nblk + G - 1) / G;
   const int per = (chunks + a.splits - 1) / a.splits;
   const int c_end = min(chunks, (split + 1) * per);
@@ -484,15 +537,15 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
   };
   auto pages = [&](int ch, int32_t (&pg)[G]) {
 #pragma unroll
-    for (int b = 0; b < G; ++b) pg[b] = table[min(ch * G + b, nblk - 1) >> page_blocks];
+    for (int b = 0; b < G; ++b) pg[b] = table[walk.block(min(ch * G + b, nblk - 1)) >> page_blocks];
   };
   auto chunk = [&](int ch, const int32_t (&pg)[G]) {
     Chunk c;
     c.all_there = true;
 #pragma unroll
     for (int b = 0; b < G; ++b) {
-      const int blk = ch * G + b;
-      const bool there = blk < nblk && pg[b] >= 0 && pg[b] < a.c.n_pages;
+      const int blk = walk.block(ch * G + b);
+      const bool there = ch * G + b < nblk && pg[b] >= 0 && pg[b] < a.c.n_pages;
       const int64_t off = kv4_block_off<D>(a.c, there ? pg[b] : 0, kvh, blk & ((1 << page_blocks) - 1));
       const uint8_t* at = a.c.data + (there ? off : 0);
       c.at[b] = at;
@@ -565,13 +618,14 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
             }
 #pragma unroll
       for (int b = 0; b < G; ++b) load_k<D>(next.at[b], lane, k[b]);
-      const int t0 = (ch * G + copy) * kKv4Block + 4 * g;
+      const int t0 = walk.block(ch * G + copy) * kKv4Block + 4 * g;
       half8_t pf[kParts][NG];
       if constexpr (edge.value) {
-        const Params<D> seen = drop_tail<D>(pr, t0, now.mine_there ? sr.len : 0);
-        softmax_step<D, true, kTwo>(acc, c, RawParams<D>{seen, unit}, sumq, t0, now.mine_there ? lim : 0, pf);
+        const Params<D> seen = drop_unseen<D, kWin>(pr, walk, t0, now.mine_there ? sr.len : 0);
+        softmax_step<D, true, kTwo, kWin>(acc, c, RawParams<D>{seen, unit}, sumq, t0,
+                                          Sees<kWin>{now.mine_there ? sees.lim : 0, sees.low, sees.sinks}, pf);
       } else {
-        softmax_step<D, false, kTwo>(acc, c, RawParams<D>{pr, unit}, sumq, t0, lim, pf);
+        softmax_step<D, false, kTwo, kWin>(acc, c, RawParams<D>{pr, unit}, sumq, t0, sees, pf);
       }
       load_p<D>(next.mine, g, pr);
 #pragma unroll
@@ -604,9 +658,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
       now = next;
       next = chunk(min(ch + 2 * kAttnWaves, c_end - 1), pg);
     };
-    const int whole = lim_lo / (G * kKv4Block);  // chunks that every row sees all of
+    const int whole = (walk.whole + G - 1) / G, whole_end = walk.whole_end / G;  // chunks that every row sees all of
     int ch = c_begin;
-    for (; ch < min(whole, c_end) && now.all_there; ch += kAttnWaves) step(ch, std::false_type{});
+    if constexpr (kWin)
+      for (; ch < min(whole, c_end); ch += kAttnWaves) step(ch, std::true_type{});
+    for (; ch < min(whole_end, c_end) && now.all_there; ch += kAttnWaves) step(ch, std::false_type{});
     for (; ch < c_end; ch += kAttnWaves) step(ch, std::true_type{});
   }
 
@@ -662,7 +718,7 @@ struct RowsBuf {
   float par[4 * (D / 64)][kKv4Block];  // [group, kind][lane group's eight tokens in turn]
 };
 
-template <int D, int DT, int R>
+template <int D, int DT, int R, bool kWin>
 __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs a) {
   using L = Kv4Layout<D>;
   constexpr int NG = D / 64, KS = D / 32, NT = D / 16;
@@ -682,17 +738,18 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
   if (wg0 >= rows) return;
   const int row0 = wg0 + wave * 16 * R;
   const bool has_rows = row0 < rows;  // a wave without rows still unpacks
-  auto limit = [&](int row) { return max(min(sr.len - sr.n + a.by_group(row) + 1, sr.len), 0); };
-  const int lim_lo = limit(wg0), lim_hi = limit(min(wg0 + kRows, rows) - 1);
-  const int wave_hi = limit(min(row0 + 16 * R, rows) - 1);
+  auto limit = [&](int row) { return sr.len - sr.n + a.by_group(row) + 1; };
+  const Walk<kWin> walk(a, limit(wg0), limit(min(wg0 + kRows, rows) - 1), sr.len);
+  const int wave_hi = max(min(limit(min(row0 + 16 * R, rows) - 1), sr.len), 0);
+  const int wave_low = kWin ? max(limit(min(row0, rows - 1)), 0) - a.window : 0;
 
-  const int nblk = (lim_hi + kKv4Block - 1) / kKv4Block;
+  const int nblk = walk.n;
   const int per = (nblk + a.splits - 1) / a.splits;
   const int b_begin = split * per, b_end = min(nblk, b_begin + per);
   const int page_blocks = a.c.page_shift - 5;
   const SHERRY_GLOBAL int32_t* table = gmem(a.table) + static_cast<int64_t>(seq) * a.table_stride;
   auto block = [&](int at, bool& there) {  // one that is not there reads the cache's first
-    const int b = min(at, b_end - 1);      // (past the last: the last again)
+    const int b = walk.block(min(at, b_end - 1));  // (past the last: the last again)
     const int32_t pg = table[b >> page_blocks];
     there = pg >= 0 && pg < a.c.n_pages;
     const int64_t off = kv4_block_off<D>(a.c, there ? pg : 0, kvh, b & ((1 << page_blocks) - 1));
@@ -731,12 +788,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
       to.v[2 * share + 1][lane] = __builtin_bit_cast(u32x4_t, v_operand<true>(vw.x, vw.y));
     }
     if (does_p) {
-      // tokens past the sequence may hold anything: their parameters are 0
-      const int tok = b * kKv4Block + 16 * ((idx >> 2) & 1) + 4 * (idx >> 3) + (idx & 3);
+      // tokens that no row sees may hold anything: their parameters are 0
+      const int tok = walk.block(b) * kKv4Block + 16 * ((idx >> 2) & 1) + 4 * (idx >> 3) + (idx & 3);
       const float x = static_cast<float>(__builtin_bit_cast(_Float16, p0));
       const float s = static_cast<float>(__builtin_bit_cast(_Float16, p1));
       const float v = kind & 1 ? __builtin_fmaf(s, kind == 1 ? -kBase : kMid, x) : (kind == 0 ? x * unit : x);
-      to.par[(threadIdx.x >> 7) * 4 + kind][idx] = tok < sr.len ? v : 0.0f;
+      to.par[(threadIdx.x >> 7) * 4 + kind][idx] = walk.seen(tok, sr.len) ? v : 0.0f;
     }
   };
   bool now_there = false, next_there = false;
@@ -744,12 +801,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
 
   u32x4_t q[R][KS];
   float sumq[R][NG];
-  int lim[R];
+  Sees<kWin> sees[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int row = min(row0 + 16 * r + col, rows - 1);
     const int tok = a.by_group(row), head = kvh * a.group + (row - tok * a.group);
-    lim[r] = sr.len - sr.n + tok + 1;
+    sees[r] = sees_of<kWin>(a, sr.len - sr.n + tok + 1);
     Queries<D, DT> f;
     f.load(a.q, (sr.first + tok) * a.q_st + head * a.q_sh + 8 * g);
     f.sums(unit, sumq[r]);
@@ -771,7 +828,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
   auto step = [&](int b, auto edge) {
     const int turn = b - b_begin;
     const RowsBuf<D>& from = lds[turn & 1];
-    if (now_there && has_rows && (!edge.value || b * kKv4Block < wave_hi)) {
+    const int t_blk = walk.block(b) * kKv4Block;
+    const bool mine = !edge.value || (t_blk < wave_hi && (!kWin || t_blk + kKv4Block > wave_low || t_blk < walk.sinks));
+    if (now_there && has_rows && mine) {
       f32x4_t c[R][2][NG];
 #pragma unroll
       for (int i = 0; i < NG; ++i)
@@ -787,11 +846,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
             for (int r = 0; r < R; ++r) c[r][t][i] = mfma_k<DT>(k, qi[r], e ? c[r][t][i] : f32x4_t{0, 0, 0, 0});
           }
         }
-      const int t0 = b * kKv4Block + 4 * g;
+      const int t0 = t_blk + 4 * g;
       half8_t pf[R][1][NG];
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        softmax_step<D, edge.value, false>(acc[r], c[r], LdsParams<D>{&from.par[0][8 * g]}, sumq[r], t0, lim[r], pf[r]);
+        softmax_step<D, edge.value, false, kWin>(acc[r], c[r], LdsParams<D>{&from.par[0][8 * g]}, sumq[r], t0, sees[r], pf[r]);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const half8_t v = __builtin_bit_cast(half8_t, from.v[i][lane]);
@@ -806,9 +865,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
       __syncthreads();
     }
   };
-  const int whole = lim_lo / kKv4Block;  // blocks that every row sees all of
   int b = b_begin;
-  for (; b < min(whole, b_end); ++b) step(b, std::false_type{});
+  if constexpr (kWin)
+    for (; b < min(walk.whole, b_end); ++b) step(b, std::true_type{});
+  for (; b < min(walk.whole_end, b_end); ++b) step(b, std::false_type{});
   for (; b < b_end; ++b) step(b, std::true_type{});
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -900,15 +960,15 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(AttnArgs a, int 
   store_row<D, DT>(one, 0, token, hd, 4 * lane, o, m, l);
 }
 
-template <int D, int DT>
+template <int D, int DT, bool kWin>
 hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.splits) * a.n_seqs * a.row_tiles * a.c.n_kv_heads));
   const dim3 block(kAttnThreads);
-  if (a.tile_rows == 8) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 2>), grid, block, 0, stream, a);
-  else if (a.tile_rows == 16) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 1>), grid, block, 0, stream, a);
-  else if (a.tile_rows == 16 * kAttnWaves) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 1>), grid, block, 0, stream, a);
-  else if (a.tile_rows == 32 * kAttnWaves) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 2>), grid, block, 0, stream, a);
-  else if constexpr (D == 64) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 4>), grid, block, 0, stream, a);
+  if (a.tile_rows == 8) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 2, kWin>), grid, block, 0, stream, a);
+  else if (a.tile_rows == 16) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 1, kWin>), grid, block, 0, stream, a);
+  else if (a.tile_rows == 16 * kAttnWaves) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 1, kWin>), grid, block, 0, stream, a);
+  else if (a.tile_rows == 32 * kAttnWaves) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 2, kWin>), grid, block, 0, stream, a);
+  else if constexpr (D == 64) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 4, kWin>), grid, block, 0, stream, a);
   if (a.splits > 1) {
     int sg = 0;
     while (sg < (D == 64 ? 4 : 3) && (2 << sg) <= a.splits) ++sg;
@@ -938,11 +998,11 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
 //     4096 of 4096   149 / 121 / 169                4096 of 4096   248 / 247
 //     128 of 4096    27 / 30 / 33                   128 of 4096    39 / 39
 //     2048 of 8192   254 / 253 / 219                512 of 8192    156 / 130
-int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv) {
+int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv, int64_t most) {
   if (rows <= 16) return rows <= 8 ? 8 : 16;
   constexpr int32_t one = 16 * kAttnWaves;
   const int64_t tiles = (rows + one - 1) / one * heads;
-  const int64_t seen = std::max(max_kv - max_q / 2, max_q / 2);
+  const int64_t seen = std::min(std::max(max_kv - max_q / 2, max_q / 2), most);
   if (rows <= one || tiles <= 128 || (seen < 1664 && tiles * head_dim < 1536 * 64)) return one;
   if (head_dim == 128 || rows <= 2 * one || seen < 3328 || tiles < 512) return 2 * one;
   return 4 * one;
@@ -985,8 +1045,13 @@ int32_t kv4_attn_splits(int32_t tile_rows, int64_t workgroups, int64_t max_kv) {
 }
 
 hipError_t launch_kv4_attn(const AttnArgs& a, int head_dim, int dt, hipStream_t stream) {
-  if (head_dim == 64) return dt == kActF16 ? launch_d<64, kActF16>(a, stream) : launch_d<64, kActBf16>(a, stream);
-  return dt == kActF16 ? launch_d<128, kActF16>(a, stream) : launch_d<128, kActBf16>(a, stream);
+  auto go = [&](auto win) {
+    constexpr bool kWin = decltype(win)::value;
+    if (head_dim == 64)
+      return dt == kActF16 ? launch_d<64, kActF16, kWin>(a, stream) : launch_d<64, kActBf16, kWin>(a, stream);
+    return dt == kActF16 ? launch_d<128, kActF16, kWin>(a, stream) : launch_d<128, kActBf16, kWin>(a, stream);
+  };
+  return a.window > 0 ? go(std::true_type{}) : go(std::false_type{});
 }
 
 }  // namespace sherry

@@ -241,6 +241,29 @@ hipError_t launch_tern3_encode(const int8_t* t, int64_t n, int64_t k, int64_t ld
 hipError_t launch_tern2_encode(const int8_t* t, int64_t n, int64_t k, int64_t ldt, uint32_t* codes,
                                hipStream_t stream);
 
+// Rows to int8 with a scale each (rowq.hip): the residual's addition and an RMS
+// norm, and the gated activation.
+struct NormQuantArgs {
+  const void* x;
+  const void* r;  // nullable: no residual
+  void* r_out;
+  const float* w;
+  int8_t* q;
+  float* scales;
+  int64_t m, k, ldx, ldr, ldro, ldq;
+  float eps;
+};
+hipError_t launch_rms_norm_quant(const NormQuantArgs& a, int xdt, int rdt, hipStream_t stream);
+constexpr int kGateSilu = 0, kGateGeluTanh = 1;
+struct GatedQuantArgs {
+  const void* gate;
+  const void* up;
+  int8_t* q;
+  float* scales;
+  int64_t m, k, ldg, ldu, ldq;
+  int32_t act;
+};
+hipError_t launch_gated_quant(const GatedQuantArgs& a, int dt, hipStream_t stream);
 
 // Norms and rotation of query and key heads (rope.hip).  A head takes
 // 1 << lph_shift lanes of 16 values.
@@ -284,6 +307,10 @@ struct Kv4Rows {
   int64_t n;
 };
 hipError_t launch_kv4_rows(const Kv4Geom& g, int head_dim, const Kv4Rows& r, int dt, bool write, hipStream_t stream);
+// Norms and rotation of q and k, k and v into the cache (kv4_append.hip): a.k
+// without an output, r.v and r.slots.
+hipError_t launch_kv4_append(const Kv4Geom& g, int head_dim, const RopeArgs& a, const Kv4Rows& r, int xdt, int ydt,
+                             hipStream_t stream);
 
 // n / d for 0 <= n < 2^31 by a multiplication (Granlund and Montgomery, Division by
 // Invariant Integers using Multiplication, 1994): the quotient is
@@ -322,11 +349,14 @@ struct AttnArgs {
   int32_t splits;
   int32_t tile_rows;      // rows of a workgroup
   int32_t row_tiles;      // workgroups that share the rows, max_q tokens x group
+  int32_t window;         // tokens up to its own that a row sees; 0: all of them
+  int32_t sinks;          // first tokens that a row with a window sees all the same
   float scale;
 };
 // Rows (tokens x query heads of one key head) that a workgroup takes, and the
-// shares that a sequence's cached tokens are split into.
-int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv);
+// shares that a sequence's cached tokens are split into.  `most`: what a row sees
+// at most (with a window).
+int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv, int64_t most);
 int32_t kv4_attn_splits(int32_t tile_rows, int64_t workgroups, int64_t max_kv);
 hipError_t launch_kv4_attn(const AttnArgs& a, int head_dim, int dt, hipStream_t stream);
 

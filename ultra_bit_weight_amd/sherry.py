@@ -1,5 +1,5 @@
-"""Thin binding over libsherry.so (C ABI in include/sherry.h): ctypes, and for the
-attention entry points the same checks in C++ (csrc/bind.cpp).
+"""Thin binding over libsherry.so (C ABI in include/sherry.h): ctypes, and for what
+a layer runs between its products the same checks in C++ (csrc/bind.cpp).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of libsherry.so.  Tensors are torch tensors on the current HIP device;
@@ -27,14 +27,14 @@ STATUS = {0: "SHERRY_OK", 1: "SHERRY_EINVAL", 2: "SHERRY_ESHAPE", 3: "SHERRY_EDT
 
 EXPORTS = [
     "sherry_version", "sherry_status_str", "sherry_packed_bytes", "sherry_pack", "sherry_decode", "sherry_gemv",
-    "sherry_act_quant", "sherry_gemv_quant",
+    "sherry_act_quant", "sherry_rms_norm_quant", "sherry_gated_quant", "sherry_gemv_quant",
     "sherry_gemv_plan_bytes", "sherry_gemv_plan", "sherry_gemv_plan_mfma", "sherry_gemv_grouped",
     "sherry_gemv_grouped_noalloc", "sherry_gemm",
     "sherry_gemm_plan_bytes", "sherry_gemm_plan", "sherry_gemm_grouped",
     "tern2_packed_bytes", "tern2_pack", "tern2_encode", "tern2_gemv", "tern2_gemv_plan", "tern2_gemm", "tern2_gemm_plan",
     "tern3_packed_bytes", "tern3_encode", "tern3_gemv", "tern3_gemv_plan_bytes", "tern3_gemv_plan",
-    "sherry_qk_norm_rope", "sherry_kv4_bytes", "sherry_kv4_write", "sherry_kv4_read", "sherry_kv4_attn_workspace",
-    "sherry_kv4_attn",
+    "sherry_qk_norm_rope", "sherry_kv4_bytes", "sherry_kv4_write", "sherry_kv4_read", "sherry_kv4_append",
+    "sherry_kv4_attn_workspace", "sherry_kv4_attn", "sherry_kv4_attn_window_workspace", "sherry_kv4_attn_window",
     "sherry_probe_read", "sherry_probe_rates", "sherry_probe_clock", "sherry_set_prefill_kernel",
 ]
 
@@ -155,6 +155,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sherry_kv4_attn.restype = i
     lib.sherry_kv4_attn.argtypes = [cp, vp, i, i64, i32, i64, i64, vp, i32, i32, i64, vp, i32, i64, vp, f, vp, i64, i64,
                                     vp, vp, sz, vp]
+    lib.sherry_kv4_attn_window_workspace.restype = sz
+    lib.sherry_kv4_attn_window_workspace.argtypes = [cp, i64, i32, i32, i32, i64, i64, i64]
+    lib.sherry_kv4_attn_window.restype = i
+    lib.sherry_kv4_attn_window.argtypes = [cp, vp, i, i64, i32, i64, i64, vp, i32, i32, i64, vp, i32, i64, vp, f, i64, i64,
+                                           vp, i64, i64, vp, vp, sz, vp]
+    lib.sherry_kv4_append.restype = i
+    lib.sherry_kv4_append.argtypes = [cp, hp, hp, vp, i64, i64, i, i, i64, i32, i32, vp, vp, i64, vp, f, vp, vp]
+    lib.sherry_rms_norm_quant.restype = i
+    lib.sherry_rms_norm_quant.argtypes = [vp, i, i64, i64, i64, vp, i64, vp, i64, i, vp, f, vp, i64, vp, vp]
+    lib.sherry_gated_quant.restype = i
+    lib.sherry_gated_quant.argtypes = [vp, i64, vp, i64, i, i64, i64, i, vp, i64, vp, vp]
     lib.sherry_set_prefill_kernel.restype = i
     lib.sherry_set_prefill_kernel.argtypes = [i]
     _lib = lib
@@ -162,7 +173,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def _load_bind():
-    """The checks of the attention entry points (csrc/bind.cpp) over the library."""
+    """The checks of csrc/bind.cpp over the library."""
     global _bind
     _need_built(_BIND_PATH)
     spec = importlib.util.spec_from_file_location("_sherry_bind", _BIND_PATH)
@@ -594,7 +605,7 @@ class GroupedGemm:
         _check("sherry_gemm_grouped", load().sherry_gemm_grouped(self.host.data_ptr(), self.dev.data_ptr(), _stream()))
 
 
-# ---- attention on a 4-bit key/value cache ----
+# ---- between a decoder layer's products ----
 
 def _launch(fn_name, dev, *args):
     """The call on device `dev` (an index) and its current stream, whichever
@@ -611,6 +622,46 @@ def _launch(fn_name, dev, *args):
             status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         _check("sherry_" + fn_name, status)
+
+
+def _quant_outs(x, q_out, scale_out):
+    if q_out is None:
+        q_out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    if scale_out is None:
+        scale_out = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
+    return q_out, scale_out
+
+
+def rms_norm_quant(x, weight, residual=None, eps=1e-6, residual_out=None, q_out=None, scale_out=None):
+    """RMS norm of x + residual with int8 codes and a scale per token, the x of the
+    int8 products, in one launch (sherry_rms_norm_quant).
+
+    x [m, k] (fp32, fp16 or bf16, unit column stride), weight fp32 [k], residual
+    [m, k] of a type of its own or None; residual_out (the sum in the residual's
+    type) may be residual itself.  Returns (codes int8 [m, k], scales fp32 [m],
+    residual_out or None)."""
+    q_out, scale_out = _quant_outs(x, q_out, scale_out)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
+    _launch("rms_norm_quant", x.get_device(), x, weight, residual, eps, residual_out, q_out, scale_out)
+    return q_out, scale_out, residual_out
+
+
+GATES = {"silu": 0, "gelu_tanh": 1}
+
+
+def gated_quant(gate, up, activation="silu", q_out=None, scale_out=None):
+    """act(gate) * up with int8 codes and a scale per token, the x of the down
+    product, in one launch (sherry_gated_quant).
+
+    gate, up [m, k] (fp32, fp16 or bf16, unit column stride: the two halves of a
+    gate|up product are taken as they lie); activation "silu" or "gelu_tanh".
+    Returns (codes int8 [m, k], scales fp32 [m])."""
+    if activation not in GATES:
+        raise ValueError(f"activation must be one of {sorted(GATES)}, got {activation!r}")
+    q_out, scale_out = _quant_outs(gate, q_out, scale_out)
+    _launch("gated_quant", gate.get_device(), gate, up, GATES[activation], q_out, scale_out)
+    return q_out, scale_out
 
 
 def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out_dtype=None,
@@ -682,19 +733,39 @@ _ANY_KV = 1 << 30  # the need grows with max_kv, up to this
 KV4_ATTN_WORKSPACE_MAX = 66 << 20  # bytes that serve every call whose tokens are at most n_seqs * max_q
 
 
-def kv4_attn_workspace(cache, n_tokens, n_q_heads, n_seqs, max_q=None, max_kv=None):
-    """A workspace for kv4_attn calls of these sizes (sherry_kv4_attn_workspace);
-    calls that may run at the same time need one each.  Without max_q it serves
+def kv4_append(cache, q, k, v, cos, sin, positions, slots, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+               out_dtype=None, q_out=None):
+    """qk_norm_rope of q and k and kv4_write of k and v in one launch, the k in
+    between in fp32 (sherry_kv4_append).
+
+    q [n, heads, head_dim] or None, k and v [n, kv_heads, head_dim] (fp32, fp16 or
+    bf16, any token and head strides), the rest as in those calls; a token whose
+    slot or position is out of range is not written.  Returns the rotated q (None
+    without q)."""
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+    elif q_out is not None and out_dtype is not None and q_out.dtype != out_dtype:
+        raise ValueError(f"q_out has dtype {q_out.dtype}, expected {out_dtype}")
+    _launch("kv4_append", cache.device, cache.address, cache.device, q, k, v, cos, sin, positions, slots, q_weight,
+            k_weight, eps, interleaved, q_out)
+    return q_out
+
+
+def kv4_attn_workspace(cache, n_tokens, n_q_heads, n_seqs, max_q=None, max_kv=None, window=None, sinks=0):
+    """A workspace for kv4_attn calls of these sizes (sherry_kv4_attn_workspace, with
+    a window sherry_kv4_attn_window_workspace); calls that may run at the same time need one each.  Without max_q it serves
     calls without max_q, without max_kv any max_kv.  A smaller batch can need more
     than a larger one: a program of changing batches asks for each, or holds
     KV4_ATTN_WORKSPACE_MAX bytes."""
-    nbytes = max(load().sherry_kv4_attn_workspace(cache.desc, n_tokens, n_q_heads, n_seqs, q, _ANY_KV if max_kv is None else max_kv)
+    lib, kv = load(), _ANY_KV if max_kv is None else max_kv
+    f, more = (lib.sherry_kv4_attn_workspace, ()) if window is None else (lib.sherry_kv4_attn_window_workspace, (window, sinks))
+    nbytes = max(f(cache.desc, n_tokens, n_q_heads, n_seqs, q, kv, *more)
                  for q in ((1, n_tokens) if max_q is None else (max_q,)))
     return torch.empty(nbytes, dtype=torch.uint8, device=cache.data.device)
 
 
 def kv4_attn(cache, q, page_table, kv_lens, cu_q=None, max_q=None, max_kv=None, scale=None, out=None, lse=None,
-             want_lse=False, workspace=None):
+             want_lse=False, workspace=None, window=None, sinks=0):
     """Causal attention of new tokens q [n, heads, head_dim] (fp16 or bf16) over
     the cache (sherry_kv4_attn): sequence s has the tokens cu_q[s] ..
     cu_q[s + 1] - 1 (int32 [n_seqs + 1]; without it max_q tokens each), its
@@ -703,6 +774,9 @@ def kv4_attn(cache, q, page_table, kv_lens, cu_q=None, max_q=None, max_kv=None, 
     the new tokens of a sequence (default: 1, with cu_q all of q's; a tight bound
     makes a smaller launch), max_kv (default: what the table holds) sizes the
     launch, scale defaults to head_dim ** -0.5.  A row that sees nothing is zeros.
+    With a window, the token at position p of its sequence sees token j <= p if
+    j > p - window or j < sinks (sherry_kv4_attn_window); pages that no row sees are
+    not read, whatever the table says of them.
     Rows of no sequence (with cu_q) are left as they were in an `out` or `lse`
     given, and are like rows that see nothing in one made here.  Returns (out, lse
     fp32 [n, heads] or None)."""
@@ -720,7 +794,7 @@ def kv4_attn(cache, q, page_table, kv_lens, cu_q=None, max_q=None, max_kv=None, 
         if q.dim() != 3 or page_table.dim() != 2:
             raise ValueError(f"q must be [tokens, heads, head_dim] and page_table [n_seqs, width], got shapes "
                              f"{tuple(q.shape)} and {tuple(page_table.shape)}")
-        workspace = kv4_attn_workspace(cache, q.shape[0], q.shape[1], page_table.shape[0], max_q, max_kv)
+        workspace = kv4_attn_workspace(cache, q.shape[0], q.shape[1], page_table.shape[0], max_q, max_kv, window, sinks)
     _launch("kv4_attn", cache.device, cache.address, cache.device, q, page_table, kv_lens, cu_q, max_q, max_kv,
-            cache.head_dim ** -0.5 if scale is None else scale, out, lse, workspace)
+            cache.head_dim ** -0.5 if scale is None else scale, window, sinks, out, lse, workspace)
     return out, lse
