@@ -140,7 +140,8 @@ sherry_status sherry_act_quant(const void* x, sherry_dtype x_dt, int64_t m, int6
  *   residual_out : m x k of r_dt, row stride ldro; NULL exactly if residual is.
  *                  It may be residual itself (with ldro = ldr)
  *   weight       : k fp32
- *   eps          : finite, not negative
+ *   eps          : finite, not negative (a row of zeros gives zeros, scale 1, also
+ *                  with 0)
  *   xq           : out, m x k int8, row stride ldq >= k; scales: out, m fp32
  * All aligned to their element sizes; rows of 16-byte aligned buffers with k a
  * multiple of 8 go fastest.  A row with a NaN or an infinity, or a sum past fp32,

@@ -1025,6 +1025,7 @@ sherry_status sherry_rms_norm_quant(const void* x, sherry_dtype x_dt, int64_t m,
   a.ldr = ldr;
   a.ldro = ldro;
   a.ldq = ldq;
+  a.inv_k = 1.0 / static_cast<double>(k);
   a.eps = eps;
   return launched(launch_rms_norm_quant(a, act_dt(xd), residual ? act_dt(rd) : -1, stream));
 }

@@ -222,18 +222,17 @@ struct Walk {
   int whole, whole_end;
   int head, gap;         // blocks before the gap, and blocks left out
   int low, sinks;        // no row sees tokens sinks .. low - 1
-  // lim_first, lim_last: tokens below them are seen by the first and the last row
-  __device__ __forceinline__ Walk(const AttnArgs& a, int lim_first, int lim_last, int len) {
-    const int lim_lo = max(lim_first, 0), lim_hi = max(min(lim_last, len), 0);
+  // lim_lo, lim_hi: how many tokens there are up to the first and the last row's own
+  __device__ __forceinline__ Walk(const AttnArgs& a, int lim_lo, int lim_hi) {
     n = (lim_hi + kKv4Block - 1) / kKv4Block;
-    whole = 0, whole_end = min(lim_lo, len) / kKv4Block;
+    whole = 0, whole_end = lim_lo / kKv4Block;
     head = gap = low = sinks = 0;
     if constexpr (kWin) {
       sinks = a.sinks;
       low = max(lim_lo - a.window, 0);
       head = (min(sinks, lim_hi) + kKv4Block - 1) / kKv4Block;
       gap = max(low / kKv4Block - head, 0);
-      const int low_last = max(max(lim_last, 0) - a.window, 0);  // where the last row's window begins
+      const int low_last = max(lim_hi - a.window, 0);  // where the last row's window begins
       whole = low_last <= sinks ? 0 : (low_last + kKv4Block - 1) / kKv4Block - gap;
       n -= gap;
       whole_end -= gap;
@@ -516,7 +515,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_few_kernel(AttnArgs 
   if (row0 >= rows) return;
   const int nrow = min(kRows, rows - row0);
 
-  const Walk<kWin> walk(a, sr.len - sr.n + a.by_group(row0) + 1, sr.len - sr.n + a.by_group(row0 + nrow - 1) + 1, sr.len);
+  const Walk<kWin> walk(a, max(sr.len - sr.n + a.by_group(row0) + 1, 0),
+                        max(min(sr.len - sr.n + a.by_group(row0 + nrow - 1) + 1, sr.len), 0));
   const int row = min(row0 + col % kRows, rows - 1);
   const int tok = a.by_group(row);
   const int head = kvh * a.group + (row - tok * a.group);
@@ -738,10 +738,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
   if (wg0 >= rows) return;
   const int row0 = wg0 + wave * 16 * R;
   const bool has_rows = row0 < rows;  // a wave without rows still unpacks
-  auto limit = [&](int row) { return sr.len - sr.n + a.by_group(row) + 1; };
-  const Walk<kWin> walk(a, limit(wg0), limit(min(wg0 + kRows, rows) - 1), sr.len);
-  const int wave_hi = max(min(limit(min(row0 + 16 * R, rows) - 1), sr.len), 0);
-  const int wave_low = kWin ? max(limit(min(row0, rows - 1)), 0) - a.window : 0;
+  auto limit = [&](int row) { return max(min(sr.len - sr.n + a.by_group(row) + 1, sr.len), 0); };
+  const Walk<kWin> walk(a, limit(wg0), limit(min(wg0 + kRows, rows) - 1));
+  const int wave_hi = limit(min(row0 + 16 * R, rows) - 1);
+  const int wave_low = kWin ? limit(min(row0, rows - 1)) - a.window : 0;
 
   const int nblk = walk.n;
   const int per = (nblk + a.splits - 1) / a.splits;
@@ -829,8 +829,8 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
     const int turn = b - b_begin;
     const RowsBuf<D>& from = lds[turn & 1];
     const int t_blk = walk.block(b) * kKv4Block;
-    const bool mine = !edge.value || (t_blk < wave_hi && (!kWin || t_blk + kKv4Block > wave_low || t_blk < walk.sinks));
-    if (now_there && has_rows && mine) {
+    if (now_there && has_rows &&
+        (!edge.value || (t_blk < wave_hi && (!kWin || t_blk + kKv4Block > wave_low || t_blk < walk.sinks)))) {
       f32x4_t c[R][2][NG];
 #pragma unroll
       for (int i = 0; i < NG; ++i)

@@ -251,6 +251,7 @@ struct NormQuantArgs {
   int8_t* q;
   float* scales;
   int64_t m, k, ldx, ldr, ldro, ldq;
+  double inv_k;
   float eps;
 };
 hipError_t launch_rms_norm_quant(const NormQuantArgs& a, int xdt, int rdt, hipStream_t stream);
@@ -349,9 +350,9 @@ struct AttnArgs {
   int32_t splits;
   int32_t tile_rows;      // rows of a workgroup
   int32_t row_tiles;      // workgroups that share the rows, max_q tokens x group
+  float scale;
   int32_t window;         // tokens up to its own that a row sees; 0: all of them
   int32_t sinks;          // first tokens that a row with a window sees all the same
-  float scale;
 };
 // Rows (tokens x query heads of one key head) that a workgroup takes, and the
 // shares that a sequence's cached tokens are split into.  `most`: what a row sees
