@@ -540,10 +540,11 @@ sherry_status kv4_rows_impl(const sherry_kv4_cache* cache, const void* k, const 
   return launched(launch_kv4_rows(g, cache->head_dim, r, act_dt(dt), write, stream));
 }
 
-// No row sees more than 2^30 tokens, so that is a window of everything.
-constexpr int64_t kAnyWindow = int64_t(1) << 30;
+// A window and its sinks; no row sees more than 2^30 tokens, so that is everything.
+constexpr int64_t kMaxKv = int64_t(1) << 30;
 struct Window {
-  int64_t tokens = kAnyWindow, sinks = 0;
+  bool on = false;
+  int64_t tokens = kMaxKv, sinks = 0;
 };
 
 // Launch sizes of an attention call.
@@ -559,15 +560,16 @@ sherry_status attn_sizes(const sherry_kv4_cache* cache, int64_t n_tokens, int32_
   const int64_t rows = static_cast<int64_t>(max_q) * a->group;
   if (rows > kMaxDim / 256) return SHERRY_ESHAPE;
   const int64_t heads = static_cast<int64_t>(n_seqs) * a->c.n_kv_heads;
-  max_kv = std::min(max_kv, int64_t(1) << 30);
-  // what a row sees at most, and (below) what the rows of a workgroup do together
-  const int64_t most = std::min(w.tokens, kAnyWindow) + std::min(w.sinks, kAnyWindow);
-  a->tile_rows = kv4_attn_tile_rows(rows, heads, cache->head_dim, max_q, max_kv, most);
+  max_kv = std::min(max_kv, kMaxKv);
+  a->tile_rows = w.on ? kv4_attn_window_tile_rows(rows, heads, cache->head_dim)
+                      : kv4_attn_tile_rows(rows, heads, cache->head_dim, max_q, max_kv);
   const int64_t tiles = (rows + a->tile_rows - 1) / a->tile_rows;
-  if (tiles > kMaxDim / 256 / heads) return SHERRY_ESHAPE;  // threads of the launch
+  if (tiles > kMaxDim / (w.on ? 512 : 256) / heads) return SHERRY_ESHAPE;  // threads of the launch
   a->row_tiles = static_cast<int32_t>(tiles);
   const int64_t tile_tokens = std::min<int64_t>(max_q, (a->tile_rows + a->group - 1) / a->group);
-  a->splits = kv4_attn_splits(a->tile_rows, tiles * heads, std::min(max_kv, most + tile_tokens));
+  const int64_t seen = std::min(w.tokens, kMaxKv) + std::min(w.sinks, kMaxKv) + tile_tokens;
+  a->splits = w.on ? kv4_attn_window_splits(a->tile_rows, tiles * heads, std::min(max_kv, seen))
+                   : kv4_attn_splits(a->tile_rows, tiles * heads, max_kv);
   *workspace = a->splits == 1 ? 0 : static_cast<size_t>(a->splits) * n_tokens * n_q_heads * (cache->head_dim + 2) * 4;
   return SHERRY_OK;
 }
@@ -583,6 +585,10 @@ sherry_status kv4_attn_impl(const sherry_kv4_cache* cache, const void* q, dt_t d
   size_t need = 0;
   if (sherry_status s = check_cache(cache, &a.c)) return s;
   if (!q || !table || !kv_lens || !out || table_width <= 0) return SHERRY_EINVAL;
+  if (w.on && w.tokens >= 1 && w.sinks >= 0 && w.tokens >= int64_t(table_width) * cache->page_size) {
+    max_kv = std::min(max_kv, w.tokens);  // a window of all that the table holds is none
+    w = Window{};
+  }
   if (sherry_status s = attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, max_kv, w, &a, &need)) return s;
   if (dt != SHERRY_F16 && dt != SHERRY_BF16) return SHERRY_EDTYPE;
   const int64_t d = cache->head_dim;
@@ -615,10 +621,9 @@ sherry_status kv4_attn_impl(const sherry_kv4_cache* cache, const void* q, dt_t d
   a.table_stride = table_stride;
   a.table_width = table_width;
   a.scale = scale;
-  // a window of all that the table holds is none
-  if (w.tokens < static_cast<int64_t>(table_width) * cache->page_size) {
-    a.window = static_cast<int32_t>(w.tokens);
-    a.sinks = static_cast<int32_t>(std::min(w.sinks, kAnyWindow));
+  if (w.on) {
+    a.window = static_cast<int32_t>(std::min(w.tokens, kMaxKv));
+    a.sinks = static_cast<int32_t>(std::min(w.sinks, kMaxKv));
   }
   a.by_kv_heads = FastDiv(static_cast<uint32_t>(a.c.n_kv_heads));
   a.by_splits = FastDiv(static_cast<uint32_t>(a.splits));
@@ -922,9 +927,13 @@ size_t sherry_kv4_attn_window_workspace(const sherry_kv4_cache* cache, int64_t n
   AttnArgs a{};
   size_t need = 0;
   if (n_tokens <= 0 || n_seqs <= 0 || check_cache(cache, &a.c) != SHERRY_OK) return 0;
-  if (attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, max_kv, Window{window, sinks}, &a, &need) != SHERRY_OK)
+  if (attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, max_kv, Window{true, window, sinks}, &a, &need) != SHERRY_OK)
     return 0;
-  return need;
+  // (the table may turn out to hold no more than the window)
+  size_t none = 0;
+  if (attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, std::min(max_kv, window), Window{}, &a, &none) != SHERRY_OK)
+    return 0;
+  return std::max(need, none);
 }
 
 sherry_status sherry_kv4_attn(const sherry_kv4_cache* cache, const void* q, sherry_dtype dt, int64_t n_tokens,
@@ -946,7 +955,7 @@ sherry_status sherry_kv4_attn_window(const sherry_kv4_cache* cache, const void* 
                                      int64_t out_stride_token, int64_t out_stride_head, float* lse, void* workspace,
                                      size_t workspace_bytes, hipStream_t stream) {
   return kv4_attn_impl(cache, q, raw(dt), n_tokens, n_q_heads, q_stride_token, q_stride_head, cu_q, n_seqs, max_q,
-                       max_kv, page_table, table_width, table_stride, kv_lens, scale, Window{window, sinks}, out,
+                       max_kv, page_table, table_width, table_stride, kv_lens, scale, Window{true, window, sinks}, out,
                        out_stride_token, out_stride_head, lse, workspace, workspace_bytes, stream);
 }
 

@@ -1,99 +1,148 @@
 // New tokens into the 4-bit cache: norms and rotation of q and k, k and v
-// quantised where they are used last, in one launch (what qk_norm_rope followed
-// by the cache's write does in two, without the 16-bit k between them).
+// quantised, in one launch (what qk_norm_rope followed by the cache's write does in
+// two, without the 16-bit k between them).
 //
 //   n = x rsqrt(mean(x^2) + eps) w, rotation of its first rot values   (rope.h)
 //   k and v per 64 values: z = f16(min), s = f16((max - min) / 15),
 //     c = clip(rint((x - z) / s), 0, 15)                               (kv4_rows.h)
 //
-// The first workgroups take 32 tokens of one key head each: k is normalised and
-// rotated in the lanes that hold whole pairs, and passes through LDS as fp32 to
-// the lanes that quantise, so that not a bit differs from the two steps with an
-// fp32 k between them.  The others take q as the rotation alone does.
+// Some workgroups take 32 tokens of one key head each, the others q as the rotation
+// alone does, in turn over the launch, so that the quantiser's arithmetic runs under
+// q's loads and stores.  Where all of a head rotates in half-split pairs, the lanes
+// of the rotation hold what the quantiser wants together, and k never leaves their
+// registers; otherwise it passes through LDS as fp32.  Either way not a bit differs
+// from the two steps with an fp32 k between them.
+#include <type_traits>
+
 #include "kv4_rows.h"
 #include "rope.h"
 
 namespace sherry {
 namespace {
 
-template <int D, int XDT, int YDT>
-__global__ __launch_bounds__(kKv4Threads) void kv4_append_kernel(Kv4Geom g, RopeArgs a, Kv4Rows r, int kv_blocks) {
+struct AppendArgs {
+  Kv4Geom g;
+  RopeArgs a;
+  Kv4Rows r;
+  uint32_t kv_blocks;  // workgroups of k and v,
+  uint32_t kv_share;   // (i * kv_share) >> 32 of them before workgroup i; 0: they go first
+  int32_t cut;         // tiles are cut where blocks of the cache begin
+  int32_t stream;      // q past the caches
+};
+
+// q: HPL heads a lane
+template <int D, int XDT, int YDT, int HPL>
+__device__ __forceinline__ void append_q(const AppendArgs& p, uint32_t number) {
+  constexpr int kLph = D / 16;
+  const RopeArgs& a = p.a;
+  const uint32_t unit = (number * static_cast<uint32_t>(kKv4Threads) + threadIdx.x) / kLph;
+  const uint32_t sets = (a.q.heads + HPL - 1) / HPL;
+  const uint32_t tok = unit / sets;
+  const int head = static_cast<int>((unit - tok * sets) * HPL);
+  const bool has = tok < a.n;
+  float x0[HPL][8], x1[HPL][8];
+  int d0, d1;
+  norm_rope<XDT, HPL>(a, a.q, tok, head, threadIdx.x & (kLph - 1), has, x0, x1, d0, d1);
+  if (!has) return;
+  auto store = [&](auto past) {
+#pragma unroll
+    for (int h = 0; h < HPL; ++h) {
+      if (head + h >= a.q.heads) break;
+      const int64_t to = tok * a.q.y_st + (head + h) * a.q.y_sh;
+      store8<YDT, decltype(past)::value>(a.q.y, to + d0, x0[h]);
+      store8<YDT, decltype(past)::value>(a.q.y, to + d1, x1[h]);
+    }
+  };
+  if (p.stream)
+    store(std::true_type{});
+  else
+    store(std::false_type{});
+}
+
+template <int D, int XDT, int YDT, int HPL, bool kDirect>
+__global__ __launch_bounds__(kKv4Threads) void kv4_append_kernel(AppendArgs p) {
   using L = Kv4Layout<D>;
-  constexpr int kTasks = kKv4Block * L::kGroups * 8 / kKv4Threads;
-  constexpr int kLph = D / 16;  // lanes of a head in the rotation
+  constexpr int kLph = D / 16;                                              // lanes of a head in the rotation
+  constexpr int kPlaces = kKv4Threads / 8;                                  // tokens of eight lanes each
+  static_assert(kPlaces == kKv4Block && kKv4Block * kLph <= kKv4Threads);
   constexpr int kPad = D + 4;
   __shared__ u32x4_t image[L::kBytes / 16];
-  __shared__ float lds_k[kKv4Block * kPad];
-  if (static_cast<int>(blockIdx.x) >= kv_blocks) {  // q
-    const uint32_t unit = ((blockIdx.x - kv_blocks) * static_cast<uint32_t>(kKv4Threads) + threadIdx.x) / kLph;
-    const uint32_t tok = unit / a.q.heads, head = unit - tok * a.q.heads;
-    const bool has = tok < a.n;
-    float x0[1][8], x1[1][8];
-    int d0, d1;
-    norm_rope<XDT, 1>(a, a.q, tok, head, threadIdx.x & (kLph - 1), has, x0, x1, d0, d1);
-    if (!has) return;
-    const int64_t to = tok * a.q.y_st + head * a.q.y_sh;
-    store8<YDT>(a.q.y, to + d0, x0[0]);
-    store8<YDT>(a.q.y, to + d1, x1[0]);
-    return;
-  }
-  const int number = blockIdx.x / g.n_kv_heads, head = blockIdx.x - number * g.n_kv_heads;
-  const int64_t first = tile_first(r, number);
+  __shared__ float lds_k[kDirect ? 1 : kKv4Block * kPad];
+  auto upto = [&](uint32_t i) { return min(p.kv_share ? __umulhi(i, p.kv_share) : i, p.kv_blocks); };
+  const uint32_t before = upto(blockIdx.x);
+  if (upto(blockIdx.x + 1) == before) return append_q<D, XDT, YDT, HPL>(p, blockIdx.x - before);
+  const Kv4Geom& g = p.g;
+  const RopeArgs& a = p.a;
+  const Kv4Rows& r = p.r;
+  const int number = before / g.n_kv_heads, head = before - number * g.n_kv_heads;
+  const int64_t first = p.cut ? tile_first(r, number) : static_cast<int64_t>(number) * kKv4Block;
+  const int l8 = threadIdx.x & 7, place = threadIdx.x >> 3;
+  const int64_t tok = first + place;
+  const bool there = tok >= 0 && tok < r.n;
   // a token whose position has no angles is not written
   int64_t slot = tile_slot(r, first);
   if (slot >= 0) {
     const int64_t pos = gmem(a.pos)[first + (threadIdx.x & (kKv4Block - 1))];
     if (pos < 0 || pos >= a.max_pos) slot = -1;
   }
-  const int l8 = threadIdx.x & 7;
-  float vx[kTasks][8];
+  float vx[L::kGroups][8];
 #pragma unroll
-  for (int i = 0; i < kTasks; ++i) {
-    const int u = (threadIdx.x + i * kKv4Threads) >> 3, gr = u % L::kGroups;
-    const int64_t tok = first + u / L::kGroups;
+  for (int i = 0; i < L::kGroups; ++i) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) vx[i][j] = 0.0f;
-    if (tok >= 0 && tok < r.n) load8<XDT>(r.v, tok * r.v_st + head * r.v_sh + gr * kKv4Group + 8 * l8, vx[i]);
+    if (there) load8<XDT>(r.v, tok * r.v_st + head * r.v_sh + i * kKv4Group + 8 * l8, vx[i]);
   }
-  if (threadIdx.x < kKv4Block * kLph) {
-    const int place = threadIdx.x / kLph;
-    const int64_t tok = first + place;
-    const bool has = tok >= 0 && tok < a.n;
+  float kx[L::kGroups][8];
+  {
     float x0[1][8], x1[1][8];
     int d0, d1;
-    norm_rope<XDT, 1>(a, a.k, tok, head, threadIdx.x & (kLph - 1), has, x0, x1, d0, d1);
+    if constexpr (kDirect && D == 128) {  // the two runs are run l8 of either group
+      norm_rope<XDT, 1>(a, a.k, tok, head, l8, there, x0, x1, d0, d1);
 #pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      *reinterpret_cast<f32x4_t*>(&lds_k[place * kPad + d0 + j]) = f32x4_t{x0[0][j], x0[0][j + 1], x0[0][j + 2], x0[0][j + 3]};
-      *reinterpret_cast<f32x4_t*>(&lds_k[place * kPad + d1 + j]) = f32x4_t{x1[0][j], x1[0][j + 1], x1[0][j + 2], x1[0][j + 3]};
+      for (int j = 0; j < 8; ++j) kx[0][j] = x0[0][j], kx[L::kGroups - 1][j] = x1[0][j];
+    } else if constexpr (kDirect) {  // the two runs are runs l8 % 4 and l8 % 4 + 4: each lane of a pair keeps one
+      norm_rope<XDT, 1>(a, a.k, tok, head, l8 & 3, there, x0, x1, d0, d1);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) kx[0][j] = l8 < 4 ? x0[0][j] : x1[0][j];
+    } else {
+      if (threadIdx.x < kKv4Block * kLph) {
+        const int at = threadIdx.x / kLph;
+        const int64_t kt = first + at;
+        norm_rope<XDT, 1>(a, a.k, kt, head, threadIdx.x & (kLph - 1), kt >= 0 && kt < a.n, x0, x1, d0, d1);
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          *reinterpret_cast<f32x4_t*>(&lds_k[at * kPad + d0 + j]) = f32x4_t{x0[0][j], x0[0][j + 1], x0[0][j + 2], x0[0][j + 3]};
+          *reinterpret_cast<f32x4_t*>(&lds_k[at * kPad + d1 + j]) = f32x4_t{x1[0][j], x1[0][j + 1], x1[0][j + 2], x1[0][j + 3]};
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < L::kGroups; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          const f32x4_t t = *reinterpret_cast<const f32x4_t*>(&lds_k[place * kPad + i * kKv4Group + 8 * l8 + j]);
+          kx[i][j] = t.x, kx[i][j + 1] = t.y, kx[i][j + 2] = t.z, kx[i][j + 3] = t.w;
+        }
     }
   }
   uint8_t* block = tile_block<D>(g, slot, head);
-  __syncthreads();
+  const int64_t own_slot = __shfl(slot, place);
 #pragma unroll
-  for (int i = 0; i < kTasks; ++i) {
-    const int u = (threadIdx.x + i * kKv4Threads) >> 3, gr = u % L::kGroups, place = u / L::kGroups;
-    float kx[8];
-#pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      const f32x4_t t = *reinterpret_cast<const f32x4_t*>(&lds_k[place * kPad + gr * kKv4Group + 8 * l8 + j]);
-      kx[j] = t.x, kx[j + 1] = t.y, kx[j + 2] = t.z, kx[j + 3] = t.w;
-    }
+  for (int i = 0; i < L::kGroups; ++i) {
     u32x2_t kc, vc;
     _Float16 ks, kz, vs, vz;
-    quantise8(kx, &kc, &ks, &kz);
+    quantise8(kx[i], &kc, &ks, &kz);
     quantise8(vx[i], &vc, &vs, &vz);
-    const int64_t own_slot = __shfl(slot, place);
     if (block) {
       auto* blk = reinterpret_cast<SHERRY_LDS uint8_t*>((SHERRY_LDS u32x4_t*)image);
-      put_k<D>(blk, place, gr, l8, kc, ks, kz);
-      put_v<D>(blk, place, gr, l8, vc, vs, vz);
+      put_k<D>(blk, place, i, l8, kc, ks, kz);
+      put_v<D>(blk, place, i, l8, vc, vs, vz);
     } else {
       int t;
       uint8_t* at = slot_block<D>(g, own_slot, head, &t);
       if (at) {  // (all eight lanes or none)
-        put_k<D>(gmem(at), t, gr, l8, kc, ks, kz);
-        put_v<D>(gmem(at), t, gr, l8, vc, vs, vz);
+        put_k<D>(gmem(at), t, i, l8, kc, ks, kz);
+        put_v<D>(gmem(at), t, i, l8, vc, vs, vz);
       }
     }
   }
@@ -103,42 +152,68 @@ __global__ __launch_bounds__(kKv4Threads) void kv4_append_kernel(Kv4Geom g, Rope
     *gmem(reinterpret_cast<u32x4_t*>(block) + i) = image[i];
 }
 
+// Heads of q a lane, where that leaves 1024 workgroups: 8192 tokens of 24 heads of 128
+// 39.2 us with 1, 35.0 with 2, 36.7 with 4.
+constexpr int kAppendHeads = 2;
+constexpr int64_t kAtOnce = 2560;
+
 template <int D, int XDT, int YDT>
-void launch_xy(const Kv4Geom& g, const RopeArgs& a, const Kv4Rows& r, hipStream_t stream) {
-  const int64_t kv = (r.n + 2 * kKv4Block - 2) / kKv4Block * g.n_kv_heads;
-  const int64_t q = (a.n * a.q.heads * (D / 16) + kKv4Threads - 1) / kKv4Threads;
-  hipLaunchKernelGGL((kv4_append_kernel<D, XDT, YDT>), dim3(static_cast<unsigned>(kv + q)), dim3(kKv4Threads), 0, stream,
-                     g, a, r, static_cast<int>(kv));
+void launch_xy(AppendArgs& p, hipStream_t stream) {
+  const int64_t n = p.a.n;
+  // (cut, the first tile may begin up to 31 tokens before token 0)
+  p.cut = n > 8 * kKv4Block;
+  const int64_t kv = (n + (p.cut ? 2 * kKv4Block - 2 : kKv4Block - 1)) / kKv4Block * p.g.n_kv_heads;
+  auto q_blocks = [&](int hpl) { return (n * ((p.a.q.heads + hpl - 1) / hpl) * (D / 16) + kKv4Threads - 1) / kKv4Threads; };
+  const bool many = q_blocks(kAppendHeads) >= 1024;
+  const int64_t total = kv + q_blocks(many ? kAppendHeads : 1);
+  // Where the chip holds the whole launch at once, k and v, whose way is longest, go
+  // first (2048 tokens, D = 128: 11.1 us, 12.4 evenly mixed); else they are spread over
+  // it (8192 tokens: 18.7 us, 25.1 first, D = 64; 35.3, 38.4, D = 128): a 32-bit
+  // fraction, rounded up, so that each step is 0 or 1 and all are there by the end.
+  p.kv_blocks = static_cast<uint32_t>(kv);
+  if (total > kAtOnce) p.kv_share = static_cast<uint32_t>(((static_cast<uint64_t>(kv) << 32) + total - 1) / total);
+  p.stream = n * p.a.q.heads * D * act_bytes(YDT) > kStreamBytes;
+  const dim3 grid(static_cast<unsigned>(total)), block(kKv4Threads);
+  const bool direct = p.a.rot == D && !p.a.interleaved;
+  if (many && direct)
+    hipLaunchKernelGGL((kv4_append_kernel<D, XDT, YDT, kAppendHeads, true>), grid, block, 0, stream, p);
+  else if (many)
+    hipLaunchKernelGGL((kv4_append_kernel<D, XDT, YDT, kAppendHeads, false>), grid, block, 0, stream, p);
+  else if (direct)
+    hipLaunchKernelGGL((kv4_append_kernel<D, XDT, YDT, 1, true>), grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL((kv4_append_kernel<D, XDT, YDT, 1, false>), grid, block, 0, stream, p);
 }
 
 template <int D, int XDT>
-void launch_x(const Kv4Geom& g, const RopeArgs& a, const Kv4Rows& r, int ydt, hipStream_t stream) {
+void launch_x(AppendArgs& p, int ydt, hipStream_t stream) {
   if (ydt == kActF32)
-    launch_xy<D, XDT, kActF32>(g, a, r, stream);
+    launch_xy<D, XDT, kActF32>(p, stream);
   else if (ydt == kActF16)
-    launch_xy<D, XDT, kActF16>(g, a, r, stream);
+    launch_xy<D, XDT, kActF16>(p, stream);
   else
-    launch_xy<D, XDT, kActBf16>(g, a, r, stream);
+    launch_xy<D, XDT, kActBf16>(p, stream);
 }
 
 template <int D>
-void launch_d(const Kv4Geom& g, const RopeArgs& a, const Kv4Rows& r, int xdt, int ydt, hipStream_t stream) {
+void launch_d(AppendArgs& p, int xdt, int ydt, hipStream_t stream) {
   if (xdt == kActF32)
-    launch_x<D, kActF32>(g, a, r, ydt, stream);
+    launch_x<D, kActF32>(p, ydt, stream);
   else if (xdt == kActF16)
-    launch_x<D, kActF16>(g, a, r, ydt, stream);
+    launch_x<D, kActF16>(p, ydt, stream);
   else
-    launch_x<D, kActBf16>(g, a, r, ydt, stream);
+    launch_x<D, kActBf16>(p, ydt, stream);
 }
 
 }  // namespace
 
 hipError_t launch_kv4_append(const Kv4Geom& g, int head_dim, const RopeArgs& a, const Kv4Rows& r, int xdt, int ydt,
                              hipStream_t stream) {
+  AppendArgs p{g, a, r, 0, 0, 0, 0};
   if (head_dim == 64)
-    launch_d<64>(g, a, r, xdt, ydt, stream);
+    launch_d<64>(p, xdt, ydt, stream);
   else
-    launch_d<128>(g, a, r, xdt, ydt, stream);
+    launch_d<128>(p, xdt, ydt, stream);
   return hipGetLastError();
 }
 

@@ -718,7 +718,7 @@ struct RowsBuf {
   float par[4 * (D / 64)][kKv4Block];  // [group, kind][lane group's eight tokens in turn]
 };
 
-template <int D, int DT, int R, bool kWin>
+template <int D, int DT, int R>
 __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs a) {
   using L = Kv4Layout<D>;
   constexpr int NG = D / 64, KS = D / 32, NT = D / 16;
@@ -739,17 +739,16 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
   const int row0 = wg0 + wave * 16 * R;
   const bool has_rows = row0 < rows;  // a wave without rows still unpacks
   auto limit = [&](int row) { return max(min(sr.len - sr.n + a.by_group(row) + 1, sr.len), 0); };
-  const Walk<kWin> walk(a, limit(wg0), limit(min(wg0 + kRows, rows) - 1));
+  const int lim_lo = limit(wg0), lim_hi = limit(min(wg0 + kRows, rows) - 1);
   const int wave_hi = limit(min(row0 + 16 * R, rows) - 1);
-  const int wave_low = kWin ? limit(min(row0, rows - 1)) - a.window : 0;
 
-  const int nblk = walk.n;
+  const int nblk = (lim_hi + kKv4Block - 1) / kKv4Block;
   const int per = (nblk + a.splits - 1) / a.splits;
   const int b_begin = split * per, b_end = min(nblk, b_begin + per);
   const int page_blocks = a.c.page_shift - 5;
   const SHERRY_GLOBAL int32_t* table = gmem(a.table) + static_cast<int64_t>(seq) * a.table_stride;
   auto block = [&](int at, bool& there) {  // one that is not there reads the cache's first
-    const int b = walk.block(min(at, b_end - 1));  // (past the last: the last again)
+    const int b = min(at, b_end - 1);      // (past the last: the last again)
     const int32_t pg = table[b >> page_blocks];
     there = pg >= 0 && pg < a.c.n_pages;
     const int64_t off = kv4_block_off<D>(a.c, there ? pg : 0, kvh, b & ((1 << page_blocks) - 1));
@@ -788,12 +787,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
       to.v[2 * share + 1][lane] = __builtin_bit_cast(u32x4_t, v_operand<true>(vw.x, vw.y));
     }
     if (does_p) {
-      // tokens that no row sees may hold anything: their parameters are 0
-      const int tok = walk.block(b) * kKv4Block + 16 * ((idx >> 2) & 1) + 4 * (idx >> 3) + (idx & 3);
+      // tokens past the sequence may hold anything: their parameters are 0
+      const int tok = b * kKv4Block + 16 * ((idx >> 2) & 1) + 4 * (idx >> 3) + (idx & 3);
       const float x = static_cast<float>(__builtin_bit_cast(_Float16, p0));
       const float s = static_cast<float>(__builtin_bit_cast(_Float16, p1));
       const float v = kind & 1 ? __builtin_fmaf(s, kind == 1 ? -kBase : kMid, x) : (kind == 0 ? x * unit : x);
-      to.par[(threadIdx.x >> 7) * 4 + kind][idx] = walk.seen(tok, sr.len) ? v : 0.0f;
+      to.par[(threadIdx.x >> 7) * 4 + kind][idx] = tok < sr.len ? v : 0.0f;
     }
   };
   bool now_there = false, next_there = false;
@@ -801,12 +800,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
 
   u32x4_t q[R][KS];
   float sumq[R][NG];
-  Sees<kWin> sees[R];
+  int lim[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int row = min(row0 + 16 * r + col, rows - 1);
     const int tok = a.by_group(row), head = kvh * a.group + (row - tok * a.group);
-    sees[r] = sees_of<kWin>(a, sr.len - sr.n + tok + 1);
+    lim[r] = sr.len - sr.n + tok + 1;
     Queries<D, DT> f;
     f.load(a.q, (sr.first + tok) * a.q_st + head * a.q_sh + 8 * g);
     f.sums(unit, sumq[r]);
@@ -828,9 +827,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
   auto step = [&](int b, auto edge) {
     const int turn = b - b_begin;
     const RowsBuf<D>& from = lds[turn & 1];
-    const int t_blk = walk.block(b) * kKv4Block;
-    if (now_there && has_rows &&
-        (!edge.value || (t_blk < wave_hi && (!kWin || t_blk + kKv4Block > wave_low || t_blk < walk.sinks)))) {
+    if (now_there && has_rows && (!edge.value || b * kKv4Block < wave_hi)) {
       f32x4_t c[R][2][NG];
 #pragma unroll
       for (int i = 0; i < NG; ++i)
@@ -846,11 +843,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
             for (int r = 0; r < R; ++r) c[r][t][i] = mfma_k<DT>(k, qi[r], e ? c[r][t][i] : f32x4_t{0, 0, 0, 0});
           }
         }
-      const int t0 = t_blk + 4 * g;
+      const int t0 = b * kKv4Block + 4 * g;
       half8_t pf[R][1][NG];
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        softmax_step<D, edge.value, false, kWin>(acc[r], c[r], LdsParams<D>{&from.par[0][8 * g]}, sumq[r], t0, sees[r], pf[r]);
+        softmax_step<D, edge.value, false, false>(acc[r], c[r], LdsParams<D>{&from.par[0][8 * g]}, sumq[r], t0,
+                                                  Sees<false>{lim[r], 0, 0}, pf[r]);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const half8_t v = __builtin_bit_cast(half8_t, from.v[i][lane]);
@@ -865,10 +863,9 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
       __syncthreads();
     }
   };
+  const int whole = lim_lo / kKv4Block;  // blocks that every row sees all of
   int b = b_begin;
-  if constexpr (kWin)
-    for (; b < min(walk.whole, b_end); ++b) step(b, std::true_type{});
-  for (; b < min(walk.whole_end, b_end); ++b) step(b, std::false_type{});
+  for (; b < min(whole, b_end); ++b) step(b, std::false_type{});
   for (; b < b_end; ++b) step(b, std::true_type{});
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -884,6 +881,181 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
 #pragma unroll
     for (int i = 0; i < NT; ++i) store_row<D, DT>(a, split, sr.first + tok, head, 16 * i + 4 * g, o[i], acc[r].m, acc[r].l);
   }
+}
+
+// ---- more rows with a window ----
+//
+// The same step, for W waves of one tile each.  A row sees about as much as any
+// other, so workgroups are alike and there are many: what counts is how few
+// instructions a row takes, and that enough waves are there to fill each other's
+// waits.  Eight waves (D = 64) halve the unpacking of each, and its page numbers,
+// branches and barriers: a step is two blocks, one unpacked by each half of the
+// waves.  Two or four tiles a wave share the unpacking too, but leave two waves to a
+// vector unit instead of four.  Bound by the vector unit, as without a window, and by
+// the blocks at either end of a tile's window, whose scores are tested one by one.
+// 2048 tokens of 32 heads on 8 over 8192, D = 64, us, with one / two / four tiles
+// on four waves, and with eight waves: window 1000 48.1 / 47.7 / 63.0, 42.9; 4096
+// 158 / 155 / 144, 137 (503 Tflop/s).  D = 128, five prompts of up to 1777 with a
+// window of 512: 87.2 / 94.2; eight waves 95.6, their registers spilled.
+template <int D, int DT, int W>
+__global__ __launch_bounds__(W * kWave, W == 8 ? 4 : D == 128 ? 3 : 2) void kv4_attn_window_rows_kernel(AttnArgs a) {
+  using L = Kv4Layout<D>;
+  static_assert(W == kAttnWaves || (W == 2 * kAttnWaves && D == 64));
+  constexpr int NG = D / 64, KS = D / 32, NT = D / 16;
+  constexpr int kRows = 16 * W, kPer = W / kAttnWaves;  // blocks of a step
+  __shared__ RowsBuf<D> lds[2][kPer];
+  const Place at_place = place(a);
+  const int split = at_place.split, seq = at_place.seq, kvh = at_place.head;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & (kWave - 1);
+  const int col = lane & 15, g = lane >> 4;
+  const SeqRange sr = seq_range(a, seq);
+  const int rows = min(sr.n, a.max_q) * a.group;
+  const int wg0 = at_place.tile * kRows;
+  if (wg0 >= rows) return;
+  const int row0 = wg0 + wave * 16;
+  const bool has_rows = row0 < rows;  // a wave without rows still unpacks
+  auto limit = [&](int row) { return max(min(sr.len - sr.n + a.by_group(row) + 1, sr.len), 0); };
+  const Walk<true> walk(a, limit(wg0), limit(min(wg0 + kRows, rows) - 1));
+  // the wave's rows see no token from hi on, nor those between the sinks and low
+  const int hi = limit(min(row0 + 16, rows) - 1), low = limit(min(row0, rows - 1)) - a.window;
+
+  const int per = (walk.n + a.splits - 1) / a.splits;
+  const int b_begin = split * per, b_end = min(walk.n, b_begin + per);
+  const int page_blocks = a.c.page_shift - 5;
+  const SHERRY_GLOBAL int32_t* table = gmem(a.table) + static_cast<int64_t>(seq) * a.table_stride;
+  // Page numbers of a step's blocks, read a step before its codes.  (Past the last
+  // block: the last again; a block that is not there reads the cache's first.)
+  auto pages = [&](int b, int32_t (&pg)[kPer]) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) pg[i] = table[walk.block(min(b + i, b_end - 1)) >> page_blocks];
+  };
+  auto is_page = [&](int32_t pg) { return pg >= 0 && pg < a.c.n_pages; };
+  // the wave's share: of block `sub` of a step, a pair of dwords a lane of K and of V
+  // (D = 64: of one of them), and of the parameters one value a thread
+  constexpr bool kBoth = D == 128;
+  const int sub = wave / kAttnWaves, part = wave & (kAttnWaves - 1);
+  const int share = kBoth ? part : part & 1;
+  const bool does_k = kBoth || part < 2, does_v = kBoth || part >= 2;
+  const int k_at = D == 64 ? lane * 16 + share * 8 : (share >> 1) * 1024 + lane * 16 + (share & 1) * 8;
+  const int v_at = L::kVOff + (share >> 1) * 1024 + lane * 16 + (share & 1) * 8;
+  const int thread = threadIdx.x & (kAttnThreads - 1);
+  const int kind = (thread >> 5) & 3, idx = thread & 31, group = thread >> 7;
+  const bool does_p = thread < NG * 128;
+  const int p_at = L::kPOff + group * 256 + idx * 2;
+  u32x2_t kw = {0, 0}, vw = {0, 0};
+  uint16_t p0 = 0, p1 = 0;
+  auto fetch = [&](int b, const int32_t (&pg)[kPer]) {
+    const int32_t mine = kPer == 1 || sub == 0 ? pg[0] : pg[kPer - 1];
+    const int in_page = walk.block(min(b + sub, b_end - 1)) & ((1 << page_blocks) - 1);
+    const int64_t off = is_page(mine) ? kv4_block_off<D>(a.c, mine, kvh, in_page) : 0;
+    const SHERRY_GLOBAL uint8_t* blk = gmem(static_cast<const uint8_t*>(a.c.data)) + off;
+    if (does_k) kw = *reinterpret_cast<const SHERRY_GLOBAL u32x2_t*>(blk + k_at);
+    if (does_v) vw = *reinterpret_cast<const SHERRY_GLOBAL u32x2_t*>(blk + v_at);
+    if (does_p) {
+      p0 = *reinterpret_cast<const SHERRY_GLOBAL uint16_t*>(blk + p_at + kind * 64);
+      p1 = *reinterpret_cast<const SHERRY_GLOBAL uint16_t*>(blk + p_at + (kind >> 1) * 128);  // its scale
+    }
+  };
+  const float unit = a.scale * kLog2e;
+  auto unpack = [&](int b, RowsBuf<D> (&step)[kPer]) {
+    RowsBuf<D>& to = step[kPer == 1 ? 0 : sub];
+    if (does_k) {
+      const int t = D == 64 ? share : share >> 1, gr = D == 64 ? 0 : share & 1;
+      to.k[t * KS + 2 * gr][lane] = k_plus_base<DT, false>(kw.x, kw.y);
+      to.k[t * KS + 2 * gr + 1][lane] = k_plus_base<DT, true>(kw.x, kw.y);
+    }
+    if (does_v) {
+      to.v[2 * share][lane] = __builtin_bit_cast(u32x4_t, v_operand<false>(vw.x, vw.y));
+      to.v[2 * share + 1][lane] = __builtin_bit_cast(u32x4_t, v_operand<true>(vw.x, vw.y));
+    }
+    if (does_p) {
+      // tokens that no row sees may hold anything: their parameters are 0
+      const int tok = walk.block(b + sub) * kKv4Block + 16 * ((idx >> 2) & 1) + 4 * (idx >> 3) + (idx & 3);
+      const float x = static_cast<float>(__builtin_bit_cast(_Float16, p0));
+      const float s = static_cast<float>(__builtin_bit_cast(_Float16, p1));
+      const float v = kind & 1 ? __builtin_fmaf(s, kind == 1 ? -kBase : kMid, x) : (kind == 0 ? x * unit : x);
+      to.par[group * 4 + kind][idx] = walk.seen(tok, sr.len) ? v : 0.0f;
+    }
+  };
+  int32_t now[kPer], next[kPer], later[kPer];
+  const bool any = b_begin < b_end;
+  if (any) {
+    pages(b_begin, now);
+    pages(b_begin + kPer, next);
+    fetch(b_begin, now);
+  }
+
+  u32x4_t q[KS];
+  float sumq[NG];
+  Sees<true> sees;
+  {
+    const int row = min(row0 + col, rows - 1);
+    const int tok = a.by_group(row), head = kvh * a.group + (row - tok * a.group);
+    sees = sees_of<true>(a, sr.len - sr.n + tok + 1);
+    Queries<D, DT> f;
+    f.load(a.q, (sr.first + tok) * a.q_st + head * a.q_sh + 8 * g);
+    f.sums(unit, sumq);
+#pragma unroll
+    for (int i = 0; i < KS; ++i) q[i] = f.bits(i);
+  }
+  Acc<D> acc;
+  acc.clear();
+  if (any) {
+    unpack(b_begin, lds[0]);
+    fetch(b_begin + kPer, next);
+    pages(b_begin + 2 * kPer, later);
+    __syncthreads();
+  }
+
+  auto block_step = [&](const RowsBuf<D>& from, int t_blk, auto edge) {
+    f32x4_t c[2][NG];
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          c[t][i] = mfma_k<DT>(from.k[t * KS + 2 * i + e][lane], q[2 * i + e], e ? c[t][i] : f32x4_t{0, 0, 0, 0});
+    half8_t pf[1][NG];
+    softmax_step<D, edge.value, false, true>(acc, c, LdsParams<D>{&from.par[0][8 * g]}, sumq, t_blk + 4 * g, sees, pf);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      acc.o[i] = mfma(__builtin_bit_cast(half8_t, from.v[i][lane]), pf[0][i >> 2], acc.o[i]);
+  };
+  auto step = [&](int b, int turn, auto edge) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t_blk = walk.block(b + i) * kKv4Block;
+      if (has_rows && is_page(now[i]) &&
+          (!edge.value || (b + i < b_end && t_blk < hi && (t_blk + kKv4Block > low || t_blk < a.sinks))))
+        block_step(lds[turn & 1][i], t_blk, edge);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) now[i] = next[i], next[i] = later[i];
+    if (b + kPer < b_end) {
+      unpack(b + kPer, lds[(turn + 1) & 1]);
+      fetch(b + 2 * kPer, next);
+      pages(b + 3 * kPer, later);
+      __syncthreads();
+    }
+  };
+  int b = b_begin, turn = 0;
+  for (; b < min(walk.whole, b_end); b += kPer) step(b, turn++, std::true_type{});
+  for (; b + kPer <= min(walk.whole_end, b_end); b += kPer) step(b, turn++, std::false_type{});
+  for (; b < b_end; b += kPer) step(b, turn++, std::true_type{});
+
+  acc.finish();
+  float o[NT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[i][j] = acc.value(i, j);
+  const int row = row0 + col;
+  if (row >= rows) return;
+  const int tok = a.by_group(row), head = kvh * a.group + (row - tok * a.group);
+#pragma unroll
+  for (int i = 0; i < NT; ++i) store_row<D, DT>(a, split, sr.first + tok, head, 16 * i + 4 * g, o[i], acc.m, acc.l);
 }
 
 // Joins the splits of every row.  A row takes D / 4 lanes (four values each)
@@ -966,9 +1138,15 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
   const dim3 block(kAttnThreads);
   if (a.tile_rows == 8) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 2, kWin>), grid, block, 0, stream, a);
   else if (a.tile_rows == 16) hipLaunchKernelGGL((kv4_attn_few_kernel<D, DT, 1, kWin>), grid, block, 0, stream, a);
-  else if (a.tile_rows == 16 * kAttnWaves) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 1, kWin>), grid, block, 0, stream, a);
-  else if (a.tile_rows == 32 * kAttnWaves) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 2, kWin>), grid, block, 0, stream, a);
-  else if constexpr (D == 64) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 4, kWin>), grid, block, 0, stream, a);
+  else if constexpr (kWin) {
+    if (a.tile_rows == 16 * kAttnWaves)
+      hipLaunchKernelGGL((kv4_attn_window_rows_kernel<D, DT, kAttnWaves>), grid, block, 0, stream, a);
+    else if constexpr (D == 64)
+      hipLaunchKernelGGL((kv4_attn_window_rows_kernel<D, DT, 2 * kAttnWaves>), grid, dim3(2 * kAttnThreads), 0, stream, a);
+  }
+  else if (a.tile_rows == 16 * kAttnWaves) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 1>), grid, block, 0, stream, a);
+  else if (a.tile_rows == 32 * kAttnWaves) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 2>), grid, block, 0, stream, a);
+  else if constexpr (D == 64) hipLaunchKernelGGL((kv4_attn_rows_kernel<D, DT, 4>), grid, block, 0, stream, a);
   if (a.splits > 1) {
     int sg = 0;
     while (sg < (D == 64 ? 4 : 3) && (2 << sg) <= a.splits) ++sg;
@@ -998,11 +1176,11 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
 //     4096 of 4096   149 / 121 / 169                4096 of 4096   248 / 247
 //     128 of 4096    27 / 30 / 33                   128 of 4096    39 / 39
 //     2048 of 8192   254 / 253 / 219                512 of 8192    156 / 130
-int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv, int64_t most) {
+int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv) {
   if (rows <= 16) return rows <= 8 ? 8 : 16;
   constexpr int32_t one = 16 * kAttnWaves;
   const int64_t tiles = (rows + one - 1) / one * heads;
-  const int64_t seen = std::min(std::max(max_kv - max_q / 2, max_q / 2), most);
+  const int64_t seen = std::max(max_kv - max_q / 2, max_q / 2);
   if (rows <= one || tiles <= 128 || (seen < 1664 && tiles * head_dim < 1536 * 64)) return one;
   if (head_dim == 128 || rows <= 2 * one || seen < 3328 || tiles < 512) return 2 * one;
   return 4 * one;
@@ -1042,6 +1220,23 @@ int32_t kv4_attn_splits(int32_t tile_rows, int64_t workgroups, int64_t max_kv) {
   if (max_kv >= two * (few ? 4 : 8) * step) n = two;
   if (few && max_kv >= six * 8 * step) n = six;
   return static_cast<int32_t>(n);
+}
+
+// With a window, many rows: eight waves a workgroup where the registers allow it
+// (D = 64) and that leaves a workgroup a CU (512 tokens over 2048, window 256: 18.5
+// us with eight, 12.6 with four).
+int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim) {
+  if (rows <= 16) return rows <= 8 ? 8 : 16;
+  constexpr int32_t one = 16 * kAttnWaves;
+  return head_dim == 128 || (rows + 2 * one - 1) / (2 * one) * heads < 256 ? one : 2 * one;
+}
+
+// Windows are as long as one another, so there is nothing to even out where the
+// workgroups fill the chip, and a join to save: few rows from one workgroup a CU on
+// (48 tokens, window 2048, D = 128: 29.0 us, 33.6 in two; 128, window 4096, D = 64:
+// 58.3, 63.1), more from two (512 tokens, window 1000: 31.5 with 256, 28.7 split).
+int32_t kv4_attn_window_splits(int32_t tile_rows, int64_t workgroups, int64_t max_seen) {
+  return workgroups >= (tile_rows <= 16 ? 256 : 512) ? 1 : kv4_attn_splits(tile_rows, workgroups, max_seen);
 }
 
 hipError_t launch_kv4_attn(const AttnArgs& a, int head_dim, int dt, hipStream_t stream) {

@@ -355,9 +355,11 @@ struct AttnArgs {
   int32_t sinks;          // first tokens that a row with a window sees all the same
 };
 // Rows (tokens x query heads of one key head) that a workgroup takes, and the
-// shares that a sequence's cached tokens are split into.  `most`: what a row sees
-// at most (with a window).
-int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv, int64_t most);
+// shares that a sequence's cached tokens are split into; and the same with a window
+// (max_seen: what the rows of a workgroup see together).
+int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv);
+int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim);
+int32_t kv4_attn_window_splits(int32_t tile_rows, int64_t workgroups, int64_t max_seen);
 int32_t kv4_attn_splits(int32_t tile_rows, int64_t workgroups, int64_t max_kv);
 hipError_t launch_kv4_attn(const AttnArgs& a, int head_dim, int dt, hipStream_t stream);
 
