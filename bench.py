@@ -61,6 +61,12 @@ def parse_args(argv=None):
                    help="only the decode pipeline with its attention run: per layer the rotation, the write to a "
                         "4-bit cache of its own and attention over TOKENS cached tokens between the q|k|v and o "
                         "products; eager and graph replay, prints its timing and exits")
+    p.add_argument("--f4-layers", type=int, default=0, metavar="TOKENS",
+                   help="only whole decoder layers of a 1B token over TOKENS cached tokens: residual norms to int8, "
+                        "q|k|v, cache append with rotation, attention, o, gate|up, gated activation to int8, down; "
+                        "eager and graph replay, prints its timing and exits")
+    p.add_argument("--f4-window", type=int, default=0, metavar="TOKENS",
+                   help="with --f4-layers: attention with a sliding window of TOKENS and four sinks")
     p.add_argument("--bf16-gemm-profile", action="store_true",
                    help="only the grouped bf16 few-token GEMM on the 3B layer (M = 2, 4, 8, 16) over 72 replicas; "
                         "prints their rates and exits")
@@ -650,6 +656,75 @@ def f4_decode_token_attention(torch, sherry, probs, layers, tokens, steps=50):
     return res
 
 
+def f4_decode_token_layers(torch, sherry, probs, layers, tokens, window=0, sinks=4, steps=50):
+    """A 1B token through whole decoder layers, each with weights and a cache of its
+    own: the residual's addition and norm to int8, the q|k|v product, the rotation
+    with the append to the 4-bit cache, attention over `tokens` cached tokens (with
+    `window`, a sliding one and `sinks` first tokens), o on its fp16 output, norm to
+    int8, gate|up, the gated activation to int8, down; the fp32 residual runs through
+    all of them.  Timed eager and replayed from one HIP graph (checked against eager
+    first)."""
+    dev = torch.device("cuda:0")
+    hid, ffn, hq, hkv, d, page = 2048, 8192, 32, 8, 64, 64
+    pages = -(-tokens // page)
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(6)
+    ang = torch.arange(tokens, dtype=torch.float64, device=dev)[:, None] * \
+        500000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64, device=dev) / d)
+    cos, sin = ang.cos().float(), ang.sin().float()
+    pos = torch.tensor([tokens - 1], device=dev)
+    lens = torch.tensor([tokens], dtype=torch.int32, device=dev)
+    see = dict(window=window, sinks=sinks) if window else {}
+    f16, f32, i8 = (dict(dtype=t, device=dev) for t in (torch.float16, torch.float32, torch.int8))
+    start = torch.randn(1, hid, generator=gen, **f32)
+    zero = torch.zeros(1, hid, **f16)
+    res, xq, hq8 = start.clone(), torch.empty(1, hid, **i8), torch.empty(1, ffn, **i8)
+    sx, sh = torch.empty(1, **f32), torch.empty(1, **f32)
+    parts, outs = [], [res]
+    for l in range(layers):
+        by = {p["name"]: p for p in probs if p["replica"] == l}
+
+        def matrix(*names, by=by):
+            return (torch.cat([by[nm]["codes"] for nm in names]), torch.cat([by[nm]["scales"] for nm in names]))
+        cache = sherry.Kv4Cache(pages, page, hkv, d, device=dev)
+        table = torch.randperm(pages, generator=gen, device=dev).to(torch.int32).view(1, pages)
+        every = (table[0].long()[:, None] * page + torch.arange(page, device=dev)).flatten()[:tokens]
+        sherry.kv4_write(cache, *(torch.randn(tokens, hkv, d, generator=gen, device=dev).half() for _ in range(2)), every)
+        w1, w2 = (1 + 0.1 * torch.randn(hid, generator=gen, **f32) for _ in range(2))
+        qkv, gu, down = torch.empty((hq + 2 * hkv) * d, **f16), torch.empty(2 * ffn, **f16), torch.empty(1, hid, **f16)
+        q, att = torch.empty(1, hq, d, **f16), torch.empty(1, hq, d, **f16)
+        o = sherry.PreparedGemvQuant(*matrix("o"), att.view(-1))
+        ws = sherry.kv4_attn_workspace(cache, 1, hq, 1, 1, tokens, **see)
+        parts.append((matrix("q", "k", "v"), qkv, cache, every[tokens - 1:], table, q, att, ws, o, matrix("gate", "up"), gu,
+                      matrix("down"), down, w1, w2))
+        outs += [qkv, q, att, o.y, gu, down]
+
+    def token():
+        res.copy_(start)
+        x = zero
+        for qkv_w, qkv, cache, slot, table, q, att, ws, o, gu_w, gu, down_w, down, w1, w2 in parts:
+            sherry.rms_norm_quant(x, w1, residual=res, residual_out=res, q_out=xq, scale_out=sx)
+            sherry.gemv(*qkv_w, xq[0], sx, out=qkv)
+            h = qkv.view(1, hq + 2 * hkv, d)
+            sherry.kv4_append(cache, h[:, :hq], h[:, hq:hq + hkv], h[:, hq + hkv:], cos, sin, pos, slot, q_out=q)
+            sherry.kv4_attn(cache, q, table, lens, max_kv=tokens, out=att, workspace=ws, **see)
+            o()
+            sherry.rms_norm_quant(o.y.view(1, hid), w2, residual=res, residual_out=res, q_out=xq, scale_out=sx)
+            sherry.gemv(*gu_w, xq[0], sx, out=gu)
+            g = gu.view(1, 2 * ffn)
+            sherry.gated_quant(g[:, :ffn], g[:, ffn:], q_out=hq8, scale_out=sh)
+            sherry.gemv(*down_w, hq8[0], sh, out=down[0])
+            x = down
+    out = {"layers": layers, "cached_tokens": tokens, "window": window, "sinks": sinks if window else 0}
+    mean_ms, _ = time_launches(torch, token, steps, 5)
+    out["eager_us_per_token"] = round(mean_ms * 1e3, 1)
+    gus = graph_time(torch, token, outs, replays=steps)
+    out["graph_us_per_token"] = gus
+    if isinstance(gus, float):
+        out["graph_us_per_layer"] = round(gus / layers, 2)
+    return out
+
+
 def graph_time(torch, fn, outs, replays=200):
     """Mean us per replay of fn captured in a HIP graph, after checking three
     replays (outputs cleared before each) against one eager run; a string
@@ -1052,6 +1127,10 @@ def main(argv=None):
         return 0
     if args.f4_attention > 0:
         print(json.dumps(f4_decode_token_attention(torch, sherry, probs, min(16, R), args.f4_attention)), flush=True)
+        return 0
+    if args.f4_layers > 0:
+        print(json.dumps(f4_decode_token_layers(torch, sherry, probs, min(16, R), args.f4_layers, args.f4_window)),
+              flush=True)
         return 0
     grouped = sherry.GroupedGemv(probs)
     torch.cuda.synchronize()
