@@ -591,3 +591,199 @@ def test_a_layer_together(gpu_lib):
     want = (q.astype(np.float64) @ t.T) * host(mats["down"][1]).astype(np.float64) * s[:, None]
     # a code or two may round the other way: one unit of one row's weight each
     assert np.abs(down - want).max() <= 2.0 ** -11 * np.abs(want).max() + 2.5 * s[0] * host(mats["down"][1]).max()
+
+
+# ------------------------------------------------ sizes that choose variants ---
+
+@pytest.mark.parametrize("d,rot,inter", [(64, 64, False), (128, 128, False), (64, 32, True), (128, 64, False)])
+@pytest.mark.parametrize("n,hq,hkv,at", [(300, 6, 3, 0), (777, 5, 2, 13), (1500, 40, 8, 32), (2100, 33, 3, 7), (600, 0, 2, 5)])
+def test_append_many(gpu_lib, d, rot, inter, n, hq, hkv, at):
+    """Tiles cut where blocks begin, two heads a lane (an odd head left over), k and v
+    first or spread over the launch, no q; some slots and positions out of range."""
+    say("append many", d, rot, inter, n, hq, hkv, at)
+    q, k, v, cos, sin, pos, w = append_inputs(n, max(hq, 1), hkv, d, rot, torch.bfloat16, True, 110 + d + n)
+    slots = (torch.arange(n) + at).to(DEV)
+    slots[n // 2] = -3
+    pages = (n + at) // 64 + 1
+    caches = [gpu_lib.Kv4Cache(pages, 64, hkv, d) for _ in range(2)]
+    for c in caches:
+        c.data.fill_(0xA5)
+    wrong = pos.clone()
+    wrong[n // 3] = -1
+    got = gpu_lib.kv4_append(caches[0], q if hq else None, k, v, cos, sin, wrong, slots, q_weight=w[0] if hq else None,
+                             k_weight=w[1], interleaved=inter)
+    off = slots.clone()
+    off[n // 3] = -1
+    want = two_calls(gpu_lib, caches[1], q, k, v, cos, sin, wrong, off, w, inter, torch.bfloat16)
+    torch.cuda.synchronize()
+    assert torch.equal(caches[0].data, caches[1].data)
+    if hq:
+        ok = torch.ones(n, dtype=torch.bool, device=DEV)
+        ok[n // 3] = False
+        assert torch.equal(got[ok], want[ok]) and torch.isnan(got[n // 3, :, :rot]).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d,qs,ls", [(32, 8, 64, [1100], [1500]), (64, 4, 64, [260, 9], [2000, 500]),
+                                            (48, 8, 64, [17] * 9, [400] * 9), (24, 8, 128, [300, 7], [900, 2000]),
+                                            (8, 8, 64, [2100], [2100]), (20, 1, 128, [13] * 3, [33, 700, 8])])
+@pytest.mark.parametrize("window,sinks", [(100, 0), (700, 65)])
+def test_window_many_rows_bf16(gpu_lib, hq, hkv, d, qs, ls, window, sinks):
+    say("window many rows", hq, hkv, d, qs, ls, window, sinks)
+    b = WindowBatch(gpu_lib, qs, ls, hq, hkv, d, 128, torch.bfloat16, 610 + d, window, sinks, q_scale=2.0)
+    b.check(*b.run())
+
+
+def test_window_max_q_cuts_a_sequence(gpu_lib):
+    """Of a longer sequence only the first max_q rows are computed; the others stay."""
+    say("window max_q")
+    for dims in ((8, 2, 64, [40, 3], [300, 90], 9), (16, 2, 128, [200, 60], [500, 61], 50), (64, 4, 64, [300, 9], [900, 30], 270)):
+        hq, hkv, d, qs, ls, max_q = dims
+        b = WindowBatch(gpu_lib, qs, ls, hq, hkv, d, 32, torch.float16, 650, 77, 5)
+        full, lse = b.run()
+        b.check(full, lse)
+        out, l2 = torch.full_like(full, 3.0), torch.full_like(lse, 3.0)
+        b.run(max_q=max_q, out=out, lse=l2)
+        torch.cuda.synchronize()
+        at = 0
+        for n in qs:
+            done = min(n, max_q)
+            err = (out[at:at + done].float() - full[at:at + done].float()).abs().max()
+            assert err <= 2.0 ** -9 * full.float().abs().max() and (out[at + done:at + n] == 3).all()
+            assert (l2[at + done:at + n] == 3).all()
+            at += n
+
+
+def test_window_spoiled_rows_and_huge_scores(gpu_lib):
+    """A row with a NaN spoils itself alone, and queries of 2^40 in size keep finite
+    rows: every other row stays within its bound.  (Not bit for bit: the maximum is
+    raised for the sixteen rows of a tile together, when one of them needs it, and
+    that rescales and rounds their sums anew.)"""
+    say("window spoiled rows")
+    for qs, ls in (([3] * 4, [200, 7, 90, 3]), ([70], [200])):
+        b = WindowBatch(gpu_lib, qs, ls, 8, 2, 64, 32, torch.bfloat16, 660, 50, 4)
+        o, lse = b.run()
+        b.check(o, lse)
+        sound = b.q.clone()
+        b.q[1, 3, 5] = float("nan")
+        b.q[2, 0] *= 2.0 ** 40
+        o2, lse2 = b.run()
+        torch.cuda.synchronize()
+        assert torch.isfinite(o2[2, 0]).all()
+        b.q = sound
+        for row in ((1, 3), (2, 0)):
+            o2[row], lse2[row] = o[row], lse[row]
+        b.check(o2, lse2)
+
+
+def test_window_slides_over_reused_pages(gpu_lib):
+    """A long chat in a cache that holds no more than its window: the pages behind the
+    window take the new tokens, the table says -1 for them, and every step is what
+    attention over a cache of everything gives."""
+    say("window reuse")
+    hq, hkv, d, page, window, sinks, total = 8, 2, 64, 32, 70, 4, 400
+    own = 1 + -(-window // page) + 1  # the sinks' page, and what a window can touch
+    small, big = gpu_lib.Kv4Cache(own, page, hkv, d), gpu_lib.Kv4Cache(-(-total // page), page, hkv, d)
+    k, v = make_kv(total, hkv, d, torch.float16, 670)
+    q = randn(total, hq, d, seed=671).half().to(DEV)
+    k, v = k.to(DEV), v.to(DEV)
+    free, table = list(range(own)), np.full(-(-total // page), -1, np.int32)
+    whole = torch.arange(-(-total // page), dtype=torch.int32, device=DEV).view(1, -1)
+    for t in range(total):
+        if t % page == 0:
+            behind = (t - window + 1) // page  # pages before it are behind the window
+            for p in range(1, max(1, behind)):
+                if table[p] >= 0:
+                    free.append(int(table[p]))
+                    table[p] = -1
+            table[t // page] = free.pop(0)
+        slot = torch.tensor([int(table[t // page]) * page + t % page], device=DEV)
+        gpu_lib.kv4_write(small, k[t:t + 1], v[t:t + 1], slot)
+        gpu_lib.kv4_write(big, k[t:t + 1], v[t:t + 1], torch.tensor([t], device=DEV))
+        lens = torch.tensor([t + 1], dtype=torch.int32, device=DEV)
+        args = dict(max_kv=total, want_lse=True, window=window, sinks=sinks)
+        o, lse = gpu_lib.kv4_attn(small, q[t:t + 1], torch.from_numpy(table).to(DEV)[None], lens, **args)
+        o2, lse2 = gpu_lib.kv4_attn(big, q[t:t + 1], whole, lens, **args)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2), t
+    assert torch.isfinite(o).all()
+
+
+def test_on_another_stream_and_together(gpu_lib):
+    """Two streams at once, each with calls of its own inputs, outputs and workspace,
+    against the same calls one after another."""
+    say("two streams")
+    n, hq, hkv, d = 300, 8, 2, 64
+    batches = [WindowBatch(gpu_lib, [n], [900 + 100 * i], hq, hkv, d, 32, torch.float16, 680 + i, 200, 4) for i in range(2)]
+    rows = [norm_inputs(64, 2048, torch.float16, torch.float32, 690 + i) for i in range(2)]
+    gates = [randn(64, 4096, seed=700 + i).half().to(DEV) for i in range(2)]
+    qs = [b.q.to(DEV) for b in batches]
+
+    def calls(i):
+        b = batches[i]
+        res = list(gpu_lib.kv4_attn(b.cache, qs[i], b.table, b.lens, cu_q=b.cu, max_q=n, want_lse=True, window=200, sinks=4))
+        res += list(gpu_lib.rms_norm_quant(rows[i][0], rows[i][2], residual=rows[i][1]))
+        res += list(gpu_lib.gated_quant(gates[i][:, :2048], gates[i][:, 2048:]))
+        return res
+    want = [calls(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [None, None]
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = calls(i)
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(want[i], got[i]))
+
+
+def test_rows_past_32_bits(gpu_lib):
+    """Rows whose offsets pass 2^32 bytes (a row stride, not a size), in every buffer."""
+    say("row offsets")
+    k, ld, m = 64, 1 << 30, 5
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GiB of GPU memory")
+    wide = torch.zeros((m - 1) * ld + k, dtype=torch.float16, device=DEV)
+    qw = torch.zeros((m - 1) * ld + k, dtype=torch.int8, device=DEV)
+    x, q = wide.as_strided((m, k), (ld, 1)), qw.as_strided((m, k), (ld, 1))
+    x.copy_(randn(m, k, seed=720).to(DEV))
+    r = torch.zeros((m - 1) * ld + k, dtype=torch.float32, device=DEV).as_strided((m, k), (ld, 1))
+    r.copy_(randn(m, k, seed=721).to(DEV))
+    w = torch.ones(k, device=DEV)
+    _, s, _ = check_norm(gpu_lib, x, r, w, q_out=q, residual_out=r)
+    check_gated(gpu_lib, x, x, "silu", q_out=q)
+    torch.cuda.synchronize()
+    assert not wide[k:ld].any() and not qw[k:ld].any()
+
+
+@pytest.mark.parametrize("k", [64, 1001, 40000])
+def test_norm_of_zeros_without_eps(gpu_lib, k):
+    """A row of zeros stays zeros with eps 0, among others that do not."""
+    say("zeros without eps", k)
+    x = randn(3, k, seed=730).to(DEV)
+    x[1] = 0
+    q, s, _ = gpu_lib.rms_norm_quant(x, torch.ones(k, device=DEV), eps=0.0)
+    torch.cuda.synchronize()
+    assert not q[1].any() and s[1] == 1 and q[0].any() and q[2].any()
+
+
+@pytest.mark.parametrize("k", [256, 2048, 8192, 1001])
+def test_codes_at_ties(gpu_lib, k):
+    """Quotients at and next to halves: y / s = n + 1/2 exactly, and one unit of y to
+    either side (weights 1, a = 1 by choice of the row, scale 1 by its largest)."""
+    say("ties", k)
+    half = np.arange(-126, 126) + 0.5
+    steps = np.stack([half, np.nextafter(half.astype(np.float32), np.float32(200)), np.nextafter(half.astype(np.float32), np.float32(-200))])
+    vals = steps.astype(np.float32).reshape(-1)
+    g = np.zeros((4, k), np.float32)
+    for i in range(4):
+        part = vals[i * (k - 1):(i + 1) * (k - 1)] if k < 800 else vals
+        g[i, 1:1 + len(part)] = part
+        g[i, 0] = 127.0
+    # silu of a gate of 256 is 256 itself, and powers of two leave y = g exact
+    up = torch.from_numpy(g).to(DEV)
+    q, s = gpu_lib.gated_quant(torch.full((4, k), 256.0, device=DEV), up / 256)
+    torch.cuda.synchronize()
+    assert (s == 1).all()
+    assert np.array_equal(host(q), np.clip(np.rint(g), -127, 127).astype(np.int8))
+    q2, s2 = gpu_lib.act_quant(up)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
