@@ -31,7 +31,7 @@ struct AppendArgs {
 };
 
 // q: HPL heads a lane
-template <int D, int XDT, int YDT, int HPL>
+template <int D, int XDT, int YDT, int HPL, bool kDirect>
 __device__ __forceinline__ void append_q(const AppendArgs& p, uint32_t number) {
   constexpr int kLph = D / 16;
   const RopeArgs& a = p.a;
@@ -42,7 +42,8 @@ __device__ __forceinline__ void append_q(const AppendArgs& p, uint32_t number) {
   const bool has = tok < a.n;
   float x0[HPL][8], x1[HPL][8];
   int d0, d1;
-  norm_rope<XDT, HPL>(a, a.q, tok, head, threadIdx.x & (kLph - 1), has, x0, x1, d0, d1);
+  norm_rope<XDT, HPL, true, kDirect>(a, a.q, min(static_cast<int64_t>(tok), a.n - 1), head, threadIdx.x & (kLph - 1), true,
+                                     x0, x1, d0, d1);
   if (!has) return;
   auto store = [&](auto past) {
 #pragma unroll
@@ -70,45 +71,40 @@ __global__ __launch_bounds__(kKv4Threads) void kv4_append_kernel(AppendArgs p) {
   __shared__ float lds_k[kDirect ? 1 : kKv4Block * kPad];
   auto upto = [&](uint32_t i) { return min(p.kv_share ? __umulhi(i, p.kv_share) : i, p.kv_blocks); };
   const uint32_t before = upto(blockIdx.x);
-  if (upto(blockIdx.x + 1) == before) return append_q<D, XDT, YDT, HPL>(p, blockIdx.x - before);
+  if (upto(blockIdx.x + 1) == before) return append_q<D, XDT, YDT, HPL, kDirect>(p, blockIdx.x - before);
   const Kv4Geom& g = p.g;
   const RopeArgs& a = p.a;
   const Kv4Rows& r = p.r;
   const int number = before / g.n_kv_heads, head = before - number * g.n_kv_heads;
   const int64_t first = p.cut ? tile_first(r, number) : static_cast<int64_t>(number) * kKv4Block;
   const int l8 = threadIdx.x & 7, place = threadIdx.x >> 3;
-  const int64_t tok = first + place;
-  const bool there = tok >= 0 && tok < r.n;
-  // a token whose position has no angles is not written
-  int64_t slot = tile_slot(r, first);
-  if (slot >= 0) {
-    const int64_t pos = gmem(a.pos)[first + (threadIdx.x & (kKv4Block - 1))];
-    if (pos < 0 || pos >= a.max_pos) slot = -1;
-  }
+  // Places of no token load the nearest one's values (no load behind a branch) and
+  // have no slot, as tokens whose position has no angles.
+  auto token = [&](int at) { return min(max(first + at, int64_t(0)), r.n - 1); };
+  const int at_lane = threadIdx.x & (kKv4Block - 1);
+  int64_t slot = gmem(r.slots)[token(at_lane)];
+  const int64_t pos = gmem(a.pos)[token(at_lane)];
+  const int64_t tok = token(place);
   float vx[L::kGroups][8];
 #pragma unroll
-  for (int i = 0; i < L::kGroups; ++i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) vx[i][j] = 0.0f;
-    if (there) load8<XDT>(r.v, tok * r.v_st + head * r.v_sh + i * kKv4Group + 8 * l8, vx[i]);
-  }
+  for (int i = 0; i < L::kGroups; ++i)
+    load8<XDT>(r.v, tok * r.v_st + head * r.v_sh + i * kKv4Group + 8 * l8, vx[i]);
   float kx[L::kGroups][8];
   {
     float x0[1][8], x1[1][8];
     int d0, d1;
     if constexpr (kDirect && D == 128) {  // the two runs are run l8 of either group
-      norm_rope<XDT, 1>(a, a.k, tok, head, l8, there, x0, x1, d0, d1);
+      norm_rope<XDT, 1, true, true>(a, a.k, tok, head, l8, true, x0, x1, d0, d1);
 #pragma unroll
       for (int j = 0; j < 8; ++j) kx[0][j] = x0[0][j], kx[L::kGroups - 1][j] = x1[0][j];
     } else if constexpr (kDirect) {  // the two runs are runs l8 % 4 and l8 % 4 + 4: each lane of a pair keeps one
-      norm_rope<XDT, 1>(a, a.k, tok, head, l8 & 3, there, x0, x1, d0, d1);
+      norm_rope<XDT, 1, true, true>(a, a.k, tok, head, l8 & 3, true, x0, x1, d0, d1);
 #pragma unroll
       for (int j = 0; j < 8; ++j) kx[0][j] = l8 < 4 ? x0[0][j] : x1[0][j];
     } else {
       if (threadIdx.x < kKv4Block * kLph) {
         const int at = threadIdx.x / kLph;
-        const int64_t kt = first + at;
-        norm_rope<XDT, 1>(a, a.k, kt, head, threadIdx.x & (kLph - 1), kt >= 0 && kt < a.n, x0, x1, d0, d1);
+        norm_rope<XDT, 1, true>(a, a.k, token(at), head, threadIdx.x & (kLph - 1), true, x0, x1, d0, d1);
 #pragma unroll
         for (int j = 0; j < 8; j += 4) {
           *reinterpret_cast<f32x4_t*>(&lds_k[at * kPad + d0 + j]) = f32x4_t{x0[0][j], x0[0][j + 1], x0[0][j + 2], x0[0][j + 3]};
@@ -125,6 +121,7 @@ __global__ __launch_bounds__(kKv4Threads) void kv4_append_kernel(AppendArgs p) {
         }
     }
   }
+  if (first + at_lane < 0 || first + at_lane >= r.n || pos < 0 || pos >= a.max_pos) slot = -1;
   uint8_t* block = tile_block<D>(g, slot, head);
   const int64_t own_slot = __shfl(slot, place);
 #pragma unroll
