@@ -12,6 +12,11 @@
 // of the rotation hold what the quantiser wants together, and k never leaves their
 // registers; otherwise it passes through LDS as fp32.  Either way not a bit differs
 // from the two steps with an fp32 k between them.
+//
+// Bound by HBM and, half as much, by the quantiser's arithmetic: 8192 tokens of 24 + 8
+// heads of 128 in 16 bits with norms 31-32 us, 4.6-4.7 TB/s (a large copy 5.1), the
+// vector unit 60 % busy before k's loads lost their branches; the two steps apart 24.3
+// and 14.  One token 3.2 us: a launch, and the angles' load behind the position's.
 #include <type_traits>
 
 #include "kv4_rows.h"
@@ -150,23 +155,26 @@ __global__ __launch_bounds__(kKv4Threads) void kv4_append_kernel(AppendArgs p) {
 }
 
 // Heads of q a lane, where that leaves 1024 workgroups: 8192 tokens of 24 heads of 128
-// 39.2 us with 1, 35.0 with 2, 36.7 with 4.
+// 34.9 us with 1, 31.2 with 2, 31.4 with 4; of 32 heads of 64 20.1, 18.1, 18.5.
 constexpr int kAppendHeads = 2;
 constexpr int64_t kAtOnce = 2560;
 
 template <int D, int XDT, int YDT>
 void launch_xy(AppendArgs& p, hipStream_t stream) {
   const int64_t n = p.a.n;
-  // (cut, the first tile may begin up to 31 tokens before token 0)
+  // Few tokens are scattered, and wait for one load less without the cut (one token
+  // 3.25 us, 3.32 with; 48 tokens 4.57, 4.66).  (Cut, the first tile may begin up to 31
+  // tokens before token 0.)
   p.cut = n > 8 * kKv4Block;
   const int64_t kv = (n + (p.cut ? 2 * kKv4Block - 2 : kKv4Block - 1)) / kKv4Block * p.g.n_kv_heads;
   auto q_blocks = [&](int hpl) { return (n * ((p.a.q.heads + hpl - 1) / hpl) * (D / 16) + kKv4Threads - 1) / kKv4Threads; };
   const bool many = q_blocks(kAppendHeads) >= 1024;
   const int64_t total = kv + q_blocks(many ? kAppendHeads : 1);
   // Where the chip holds the whole launch at once, k and v, whose way is longest, go
-  // first (2048 tokens, D = 128: 11.1 us, 12.4 evenly mixed); else they are spread over
-  // it (8192 tokens: 18.7 us, 25.1 first, D = 64; 35.3, 38.4, D = 128): a 32-bit
-  // fraction, rounded up, so that each step is 0 or 1 and all are there by the end.
+  // first (512 tokens, D = 128: 5.3 us, 6.2 evenly mixed; 1024, D = 64: 4.5, 5.3); else
+  // they are spread over it (8192 tokens, D = 128: 31.2 us, 32.3 first; of fp32 43.9,
+  // 46.5): a 32-bit fraction, rounded up, so that each step is 0 or 1 and all are there
+  // by the end.
   p.kv_blocks = static_cast<uint32_t>(kv);
   if (total > kAtOnce) p.kv_share = static_cast<uint32_t>(((static_cast<uint64_t>(kv) << 32) + total - 1) / total);
   p.stream = n * p.a.q.heads * D * act_bytes(YDT) > kStreamBytes;

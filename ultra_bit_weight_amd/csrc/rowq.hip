@@ -194,16 +194,16 @@ __global__ __launch_bounds__(row_block(T)) void rms_norm_quant_rows(NormQuantArg
   Raw8<4> w[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = c0 + i * T * 8;
-    if (c < k) {
-      x[i].load(a.x, row * a.ldx + c);
-      r[i].load(a.r, row * a.ldr + c);
-      w[i].load(a.w, c);
-    } else {
-      x[i].clear();
-      r[i].clear();
-      w[i].clear();
-    }
+    const int c = min(c0 + i * T * 8, k - 8);
+    x[i].load(a.x, row * a.ldx + c);
+    r[i].load(a.r, row * a.ldr + c);
+    w[i].load(a.w, c);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {  // (runs past the row's end: no load stands behind a branch)
+    if (c0 + i * T * 8 < k) continue;
+    x[i].clear();
+    r[i].clear();
   }
   float h[V][8];
   widen<XB, V>(x, xdt, h);
@@ -260,14 +260,15 @@ __global__ __launch_bounds__(row_block(T)) void gated_quant_rows(GatedQuantArgs 
   Raw8<XB> g[V], u[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = c0 + i * T * 8;
-    if (c < k) {
-      g[i].load(a.gate, row * a.ldg + c);
-      u[i].load(a.up, row * a.ldu + c);
-    } else {
-      g[i].clear();
-      u[i].clear();
-    }
+    const int c = min(c0 + i * T * 8, k - 8);
+    g[i].load(a.gate, row * a.ldg + c);
+    u[i].load(a.up, row * a.ldu + c);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (c0 + i * T * 8 < k) continue;
+    g[i].clear();
+    u[i].clear();
   }
   float y[V][8], v[V][8];
   widen<XB, V>(g, dt, y);
