@@ -787,3 +787,30 @@ def test_codes_at_ties(gpu_lib, k):
     assert np.array_equal(host(q), np.clip(np.rint(g), -127, 127).astype(np.int8))
     q2, s2 = gpu_lib.act_quant(up)
     assert torch.equal(q, q2) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("m,k", [(300, 520), (9, 2056), (40, 6152), (5, 20000)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_norm_in_place_with_idle_threads(gpu_lib, m, k, dtype):
+    """Rows shorter than their threads' runs, the residual in place, many times over."""
+    say("in place, idle threads", m, k, dtype)
+    x, r, w = norm_inputs(m, k, torch.float16, dtype, 740)
+    want = gpu_lib.rms_norm_quant(x, w, residual=r)
+    for _ in range(20):
+        mine = r.clone()
+        got = gpu_lib.rms_norm_quant(x, w, residual=mine, residual_out=mine)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("n,hq,d", [(2100, 33, 64), (1030, 41, 128), (5, 3, 64)])
+def test_append_in_place(gpu_lib, n, hq, d):
+    """q rotated where it lies, two heads a lane with one left over, many times over."""
+    say("append in place", n, hq, d)
+    q, k, v, cos, sin, pos, w = append_inputs(n, hq, 2, d, d, torch.float16, True, 750)
+    slots = torch.arange(n, device=DEV)
+    caches = [gpu_lib.Kv4Cache(n // 32 + 1, 32, 2, d) for _ in range(2)]
+    want = gpu_lib.kv4_append(caches[0], q, k, v, cos, sin, pos, slots, q_weight=w[0], k_weight=w[1])
+    for _ in range(20):
+        mine = q.clone()
+        gpu_lib.kv4_append(caches[1], mine, k, v, cos, sin, pos, slots, q_weight=w[0], k_weight=w[1], q_out=mine)
+        assert torch.equal(mine, want) and torch.equal(caches[0].data, caches[1].data)

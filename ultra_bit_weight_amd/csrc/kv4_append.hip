@@ -13,10 +13,11 @@
 // registers; otherwise it passes through LDS as fp32.  Either way not a bit differs
 // from the two steps with an fp32 k between them.
 //
-// Bound by HBM and, half as much, by the quantiser's arithmetic: 8192 tokens of 24 + 8
-// heads of 128 in 16 bits with norms 31-32 us, 4.6-4.7 TB/s (a large copy 5.1), the
-// vector unit 60 % busy before k's loads lost their branches; the two steps apart 24.3
-// and 14.  One token 3.2 us: a launch, and the angles' load behind the position's.
+// Bound by HBM, beside the quantiser's arithmetic: 8192 tokens of 24 + 8 heads of 128
+// in 16 bits with norms 31-32 us, 4.6-4.7 TB/s (a large copy 5.1), the vector unit 58 %
+// busy; the two steps apart 24.3 and 14.  One token 3.2 us: a launch, and the angles'
+// load behind the position's.  No load stands behind a branch, which the compiler
+// would wait for before the next (one token 3.75 us, 8192 36.5 with them).
 #include <type_traits>
 
 #include "kv4_rows.h"

@@ -12,8 +12,8 @@
 //
 // Bound by HBM: a row is read once and stays in its threads' registers through
 // both reductions.  T threads take a row, V runs of eight values each.  8192 rows of
-// 4096 in 16 bits with their residual 45.5 us, 5.2 TB/s, the rate of a large copy;
-// 8192 rows of gate and up, 8192 each, 61 us, 5.5 TB/s; one row 2.8 and 3.1 us, a
+// 4096 in 16 bits with their residual 44.4 us, 5.3 TB/s, the rate of a large copy;
+// 8192 rows of gate and up, 8192 each, 60 us, 5.6 TB/s; one row 2.75 and 3.15 us, a
 // launch and one load-reduce-store.
 #include <type_traits>
 
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(row_block(T)) void rms_norm_quant_rows(NormQuantArg
     w[i].load(a.w, c);
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) {  // (runs past the row's end: no load stands behind a branch)
+  for (int i = 0; i < V; ++i) {  // (runs past the row's end loaded its last, so that no load stands behind a branch)
     if (c0 + i * T * 8 < k) continue;
     x[i].clear();
     r[i].clear();
