@@ -596,7 +596,8 @@ def test_a_layer_together(gpu_lib):
 # ------------------------------------------------ sizes that choose variants ---
 
 @pytest.mark.parametrize("d,rot,inter", [(64, 64, False), (128, 128, False), (64, 32, True), (128, 64, False)])
-@pytest.mark.parametrize("n,hq,hkv,at", [(300, 6, 3, 0), (777, 5, 2, 13), (1500, 40, 8, 32), (2100, 33, 3, 7), (600, 0, 2, 5)])
+@pytest.mark.parametrize("n,hq,hkv,at", [(300, 6, 3, 0), (777, 5, 2, 13), (1500, 40, 8, 32), (2100, 33, 3, 7), (600, 0, 2, 5),
+                                          (1200, 0, 2, 5), (1025, 4, 1, 0), (1024, 4, 1, 3)])
 def test_append_many(gpu_lib, d, rot, inter, n, hq, hkv, at):
     """Tiles cut where blocks begin, two heads a lane (an odd head left over), k and v
     first or spread over the launch, no q; some slots and positions out of range."""
@@ -814,3 +815,21 @@ def test_append_in_place(gpu_lib, n, hq, d):
         mine = q.clone()
         gpu_lib.kv4_append(caches[1], mine, k, v, cos, sin, pos, slots, q_weight=w[0], k_weight=w[1], q_out=mine)
         assert torch.equal(mine, want) and torch.equal(caches[0].data, caches[1].data)
+
+
+@pytest.mark.parametrize("d,rot,inter", [(64, 64, False), (128, 128, False), (64, 16, False), (128, 96, True)])
+@pytest.mark.parametrize("n,hq,hkv", [(1030, 6, 3), (1400, 40, 10), (7, 3, 2), (250, 9, 1)])
+def test_append_scattered(gpu_lib, d, rot, inter, n, hq, hkv):
+    """Many tokens to slots in no order, of large pages, some out of range: what is
+    written between them stays."""
+    say("append scattered", d, rot, inter, n, hq, hkv)
+    q, k, v, cos, sin, pos, w = append_inputs(n, hq, hkv, d, rot, torch.float16, True, 760 + d + n)
+    cap = 256 * 8
+    slots = torch.from_numpy(HOW["skips"](n, cap, np.random.default_rng(n + d)).astype(np.int64)).to(DEV)
+    caches = [gpu_lib.Kv4Cache(8, 256, hkv, d) for _ in range(2)]
+    for c in caches:
+        c.data.fill_(0xA5)
+    got = gpu_lib.kv4_append(caches[0], q, k, v, cos, sin, pos, slots, q_weight=w[0], k_weight=w[1], interleaved=inter)
+    want = two_calls(gpu_lib, caches[1], q, k, v, cos, sin, pos, slots, w, inter, torch.float16)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(caches[0].data, caches[1].data)

@@ -15,9 +15,9 @@
 //
 // Bound by HBM, beside the quantiser's arithmetic: 8192 tokens of 24 + 8 heads of 128
 // in 16 bits with norms 31-32 us, 4.6-4.7 TB/s (a large copy 5.1), the vector unit 58 %
-// busy; the two steps apart 24.3 and 14.  One token 3.2 us: a launch, and the angles'
+// busy; the two steps apart 24.3 and 14.  One token 2.9 us: a launch, and the angles'
 // load behind the position's.  No load stands behind a branch, which the compiler
-// would wait for before the next (one token 3.75 us, 8192 36.5 with them).
+// would wait for before the next (8192 tokens 36.5 us with them).
 #include <type_traits>
 
 #include "kv4_rows.h"
@@ -32,7 +32,6 @@ struct AppendArgs {
   Kv4Rows r;
   uint32_t kv_blocks;  // workgroups of k and v,
   uint32_t kv_share;   // (i * kv_share) >> 32 of them before workgroup i; 0: they go first
-  int32_t cut;         // tiles are cut where blocks of the cache begin
   int32_t stream;      // q past the caches
 };
 
@@ -82,7 +81,7 @@ __global__ __launch_bounds__(kKv4Threads) void kv4_append_kernel(AppendArgs p) {
   const RopeArgs& a = p.a;
   const Kv4Rows& r = p.r;
   const int number = before / g.n_kv_heads, head = before - number * g.n_kv_heads;
-  const int64_t first = p.cut ? tile_first(r, number) : static_cast<int64_t>(number) * kKv4Block;
+  const int64_t first = tile_first(r, number);
   const int l8 = threadIdx.x & 7, place = threadIdx.x >> 3;
   // Places of no token load the nearest one's values (no load behind a branch) and
   // have no slot, as tokens whose position has no angles.
@@ -155,32 +154,105 @@ __global__ __launch_bounds__(kKv4Threads) void kv4_append_kernel(AppendArgs p) {
     *gmem(reinterpret_cast<u32x4_t*>(block) + i) = image[i];
 }
 
+// ---- few tokens: what counts is how long one wave's way is ----
+//
+// K and V, and the groups of 64 of a head, go to waves of their own, eight tokens
+// each, so that no wave quantises twice; each token's bytes are written where they lie.
+template <int D, int XDT, int YDT, bool kDirect>
+__global__ __launch_bounds__(kKv4Threads) void kv4_append_few_kernel(AppendArgs p) {
+  constexpr int kLph = D / 16, kPad = D + 4;
+  constexpr int kWaves = kKv4Threads / kWave, kTokens = kWave / 8;
+  constexpr int kSets = kWaves / (2 * Kv4Layout<D>::kGroups);  // of kTokens tokens
+  __shared__ float lds_k[kDirect ? 1 : kWaves][kDirect ? 1 : kTokens * kPad];
+  if (blockIdx.x >= p.kv_blocks) return append_q<D, XDT, YDT, 1, kDirect>(p, blockIdx.x - p.kv_blocks);
+  const Kv4Geom& g = p.g;
+  const RopeArgs& a = p.a;
+  const Kv4Rows& r = p.r;
+  const int number = blockIdx.x / g.n_kv_heads, head = blockIdx.x - number * g.n_kv_heads;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & (kWave - 1), place = lane >> 3, l8 = lane & 7;
+  const bool is_v = wave & 1;
+  const int gr = D == 64 ? 0 : wave >> 1;
+  const int64_t first = (static_cast<int64_t>(number) * kSets + (D == 64 ? wave >> 1 : 0)) * kTokens;
+  // (places of no token: the last one's values, and no slot)
+  auto token = [&](int at) { return min(first + at, r.n - 1); };
+  const int64_t tok = token(place);
+  int64_t slot = gmem(r.slots)[tok];
+  const int64_t pos = gmem(a.pos)[tok];
+  float x[8];
+  if (is_v) {
+    load8<XDT>(r.v, tok * r.v_st + head * r.v_sh + gr * kKv4Group + 8 * l8, x);
+  } else if (kDirect || lane < kTokens * kLph) {
+    float x0[1][8], x1[1][8];
+    int d0, d1;
+    const int at = kDirect ? place : lane / kLph;
+    norm_rope<XDT, 1, true, kDirect>(a, a.k, token(at), head, lane & (kLph - 1), true, x0, x1, d0, d1);
+    if constexpr (kDirect) {
+      // D = 128: the two runs are run l8 of either group; D = 64: runs l8 % 4 and l8 % 4 + 4
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = (D == 128 ? gr == 0 : l8 < 4) ? x0[0][j] : x1[0][j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) lds_k[wave][at * kPad + d0 + j] = x0[0][j], lds_k[wave][at * kPad + d1 + j] = x1[0][j];
+    }
+  }
+  if constexpr (!kDirect) {
+    __syncthreads();
+    if (!is_v) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = lds_k[wave][place * kPad + gr * kKv4Group + 8 * l8 + j];
+    }
+  }
+  if (first + place >= r.n || pos < 0 || pos >= a.max_pos) slot = -1;
+  u32x2_t c;
+  _Float16 s, z;
+  quantise8(x, &c, &s, &z);
+  int t;
+  uint8_t* to = slot_block<D>(g, slot, head, &t);
+  if (!to) return;  // (all eight lanes of a token or none)
+  if (is_v)
+    put_v<D>(gmem(to), t, gr, l8, c, s, z);
+  else
+    put_k<D>(gmem(to), t, gr, l8, c, s, z);
+}
+
 // Heads of q a lane, where that leaves 1024 workgroups: 8192 tokens of 24 heads of 128
 // 34.9 us with 1, 31.2 with 2, 31.4 with 4; of 32 heads of 64 20.1, 18.1, 18.5.
 constexpr int kAppendHeads = 2;
 constexpr int64_t kAtOnce = 2560;
+// Up to this the few-token kernel: 1 token of 24 + 8 heads of 128 with norms 3.27 us,
+// with the other kernel 4.36; 48 tokens 3.28, 4.57; 512 4.55, 5.28; 1000 7.27, 7.45; of
+// 32 + 8 heads of 64 2.88, 3.25 (1), 3.31, 3.67 (512), 4.29, 4.50 (1000).
+constexpr int64_t kFew = 1024;
 
 template <int D, int XDT, int YDT>
 void launch_xy(AppendArgs& p, hipStream_t stream) {
   const int64_t n = p.a.n;
-  // Few tokens are scattered, and wait for one load less without the cut (one token
-  // 3.25 us, 3.32 with; 48 tokens 4.57, 4.66).  (Cut, the first tile may begin up to 31
-  // tokens before token 0.)
-  p.cut = n > 8 * kKv4Block;
-  const int64_t kv = (n + (p.cut ? 2 * kKv4Block - 2 : kKv4Block - 1)) / kKv4Block * p.g.n_kv_heads;
+  const dim3 block(kKv4Threads);
+  const bool direct = p.a.rot == D && !p.a.interleaved;
   auto q_blocks = [&](int hpl) { return (n * ((p.a.q.heads + hpl - 1) / hpl) * (D / 16) + kKv4Threads - 1) / kKv4Threads; };
+  if (n <= kFew) {
+    constexpr int kTokens = D == 64 ? 16 : 8;
+    p.kv_blocks = static_cast<uint32_t>((n + kTokens - 1) / kTokens * p.g.n_kv_heads);
+    const dim3 grid(static_cast<unsigned>(p.kv_blocks + q_blocks(1)));
+    if (direct)
+      hipLaunchKernelGGL((kv4_append_few_kernel<D, XDT, YDT, true>), grid, block, 0, stream, p);
+    else
+      hipLaunchKernelGGL((kv4_append_few_kernel<D, XDT, YDT, false>), grid, block, 0, stream, p);
+    return;
+  }
+  // (the first tile may begin up to 31 tokens before token 0)
+  const int64_t kv = (n + 2 * kKv4Block - 2) / kKv4Block * p.g.n_kv_heads;
   const bool many = q_blocks(kAppendHeads) >= 1024;
   const int64_t total = kv + q_blocks(many ? kAppendHeads : 1);
   // Where the chip holds the whole launch at once, k and v, whose way is longest, go
-  // first (512 tokens, D = 128: 5.3 us, 6.2 evenly mixed; 1024, D = 64: 4.5, 5.3); else
-  // they are spread over it (8192 tokens, D = 128: 31.2 us, 32.3 first; of fp32 43.9,
-  // 46.5): a 32-bit fraction, rounded up, so that each step is 0 or 1 and all are there
-  // by the end.
+  // first (2048 tokens, D = 64: 7.2 us, 7.4 evenly mixed); else they are spread over it
+  // (8192 tokens, D = 128: 31.2 us, 32.3 first; of fp32 43.9, 46.5): a 32-bit fraction,
+  // rounded up, so that each step is 0 or 1 and all are there by the end.
   p.kv_blocks = static_cast<uint32_t>(kv);
   if (total > kAtOnce) p.kv_share = static_cast<uint32_t>(((static_cast<uint64_t>(kv) << 32) + total - 1) / total);
   p.stream = n * p.a.q.heads * D * act_bytes(YDT) > kStreamBytes;
-  const dim3 grid(static_cast<unsigned>(total)), block(kKv4Threads);
-  const bool direct = p.a.rot == D && !p.a.interleaved;
+  const dim3 grid(static_cast<unsigned>(total));
   if (many && direct)
     hipLaunchKernelGGL((kv4_append_kernel<D, XDT, YDT, kAppendHeads, true>), grid, block, 0, stream, p);
   else if (many)
@@ -215,7 +287,7 @@ void launch_d(AppendArgs& p, int xdt, int ydt, hipStream_t stream) {
 
 hipError_t launch_kv4_append(const Kv4Geom& g, int head_dim, const RopeArgs& a, const Kv4Rows& r, int xdt, int ydt,
                              hipStream_t stream) {
-  AppendArgs p{g, a, r, 0, 0, 0, 0};
+  AppendArgs p{g, a, r, 0, 0, 0};
   if (head_dim == 64)
     launch_d<64>(p, xdt, ydt, stream);
   else
