@@ -895,8 +895,10 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
 // the blocks at either end of a tile's window, whose scores are tested one by one.
 // 2048 tokens of 32 heads on 8 over 8192, D = 64, us, with one / two / four tiles
 // on four waves, and with eight waves: window 1000 48.1 / 47.7 / 63.0, 42.9; 4096
-// 158 / 155 / 144, 137 (503 Tflop/s).  D = 128, five prompts of up to 1777 with a
-// window of 512: 87.2 / 94.2; eight waves 95.6, their registers spilled.
+// 158 / 155 / 144, 137; and with the softmax's wave priority 41.9 and 130 (530
+// Tflop/s).  D = 128, five prompts of up to 1777 with a window of 512: 87.2 / 94.2;
+// eight waves 95.6, their registers spilled; with the priority 91.7 (though 187 for 201
+// with a window of 4096).
 template <int D, int DT, int W>
 __global__ __launch_bounds__(W * kWave, W == 8 ? 4 : D == 128 ? 3 : 2) void kv4_attn_window_rows_kernel(AttnArgs a) {
   using L = Kv4Layout<D>;
@@ -1009,6 +1011,7 @@ __global__ __launch_bounds__(W * kWave, W == 8 ? 4 : D == 128 ? 3 : 2) void kv4_
   }
 
   auto block_step = [&](const RowsBuf<D>& from, int t_blk, auto edge) {
+    constexpr bool kFirst = D == 64 && !edge.value;
     f32x4_t c[2][NG];
 #pragma unroll
     for (int i = 0; i < NG; ++i)
@@ -1018,10 +1021,13 @@ __global__ __launch_bounds__(W * kWave, W == 8 ? 4 : D == 128 ? 3 : 2) void kv4_
         for (int t = 0; t < 2; ++t)
           c[t][i] = mfma_k<DT>(from.k[t * KS + 2 * i + e][lane], q[2 * i + e], e ? c[t][i] : f32x4_t{0, 0, 0, 0});
     half8_t pf[1][NG];
+    // a wave that has its scores goes on to their product before others begin theirs
+    if constexpr (kFirst) __builtin_amdgcn_s_setprio(1);
     softmax_step<D, edge.value, false, true>(acc, c, LdsParams<D>{&from.par[0][8 * g]}, sumq, t_blk + 4 * g, sees, pf);
 #pragma unroll
     for (int i = 0; i < NT; ++i)
       acc.o[i] = mfma(__builtin_bit_cast(half8_t, from.v[i][lane]), pf[0][i >> 2], acc.o[i]);
+    if constexpr (kFirst) __builtin_amdgcn_s_setprio(0);
   };
   auto step = [&](int b, int turn, auto edge) {
 #pragma unroll
