@@ -833,3 +833,61 @@ def test_append_scattered(gpu_lib, d, rot, inter, n, hq, hkv):
     want = two_calls(gpu_lib, caches[1], q, k, v, cos, sin, pos, slots, w, inter, torch.float16)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(caches[0].data, caches[1].data)
+
+
+# ------------------------------------- rows of lengths and places of any kind ---
+
+LOOSE_SIZES = [8, 9, 12, 15, 17, 510, 513, 519, 1025, 2047, 2052, 4095, 4097, 8191, 8193, 16385, 32767]
+
+
+@pytest.mark.parametrize("k", LOOSE_SIZES)
+@pytest.mark.parametrize("x_dt,r_dt", [(torch.float16, torch.bfloat16), (torch.bfloat16, torch.float32),
+                                       (torch.float32, torch.float16), (torch.float32, torch.float32)])
+@pytest.mark.parametrize("first", [0, 1, 5])
+def test_norm_any_place(gpu_lib, k, x_dt, r_dt, first):
+    """Odd lengths from an odd place on, the residual in place, what lies around left."""
+    say("norm any place", k, x_dt, r_dt, first)
+    m, ld = 5, k + first + 2
+    x, r, w = norm_inputs(m, k, x_dt, r_dt, 1200 + k + first)
+    want = gpu_lib.rms_norm_quant(x.contiguous(), w, residual=r)
+    wide = torch.full((m, ld), 55.0, device=DEV).to(r_dt)
+    mine, xin = wide[:, first:first + k], torch.full((m, ld), 9.0, device=DEV).to(x_dt)[:, first:first + k]
+    mine.copy_(r)
+    xin.copy_(x)
+    w_in = torch.ones(k + first, device=DEV)[first:]
+    w_in.copy_(w)
+    q_wide = torch.full((m, ld), 77, dtype=torch.int8, device=DEV)
+    got = check_norm(gpu_lib, xin, mine, w_in, q_out=q_wide[:, first:first + k], residual_out=mine)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    assert (wide[:, :first] == 55).all() and (wide[:, first + k:] == 55).all()
+    assert (q_wide[:, :first] == 77).all() and (q_wide[:, first + k:] == 77).all()
+
+
+@pytest.mark.parametrize("m,k", [(2000, 513), (900, 2047), (300, 4097), (90, 16385)])
+@pytest.mark.parametrize("r_dt", [torch.float16, torch.float32])
+def test_norm_in_place_many_times(gpu_lib, m, k, r_dt):
+    """The waves of a row, whose last runs overlap, in any order."""
+    say("norm in place many times", m, k, r_dt)
+    x, r, w = norm_inputs(m, k, torch.float16, r_dt, 1300 + k)
+    want = gpu_lib.rms_norm_quant(x, w, residual=r)
+    for _ in range(10):
+        mine = r.clone()
+        got = gpu_lib.rms_norm_quant(x, w, residual=mine, residual_out=mine)
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("k", LOOSE_SIZES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("first", [0, 1, 5])
+def test_gated_any_place(gpu_lib, k, dtype, first):
+    say("gated any place", k, dtype, first)
+    m = 5
+    gu = (randn(m, 2 * k + first, seed=1400 + k) * 2).to(dtype).to(DEV)
+    q_wide = torch.full((m, k + first + 2), 77, dtype=torch.int8, device=DEV)
+    g, u = gu[:, first:first + k], gu[:, first + k:]
+    q, s = check_gated(gpu_lib, g, u, "silu", q_out=q_wide[:, first:first + k])
+    q2, s2 = gpu_lib.gated_quant(g.contiguous(), u.contiguous())
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    assert (q_wide[:, :first] == 77).all() and (q_wide[:, first + k:] == 77).all()

@@ -74,14 +74,22 @@ struct RowTeam {
   }
 };
 
-// Eight values as they lie, B bytes each.
+// A vector at addresses of A bytes' alignment.
+template <class W, int A>
+struct __attribute__((packed, aligned(A))) Vec {
+  W v;
+};
+
+// Eight values as they lie, B bytes each, aligned as 16 bytes or (kLoose) as one value.
 template <int B>
 struct Raw8 {
   u32x4_t w[B / 2];
+  template <bool kLoose>
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    const SHERRY_GLOBAL u32x4_t* at = gmem(reinterpret_cast<const u32x4_t*>(static_cast<const char*>(p) + i * B));
+    typedef Vec<u32x4_t, kLoose ? B : 16> vec_t;
+    const SHERRY_GLOBAL vec_t* at = gmem(reinterpret_cast<const vec_t*>(static_cast<const char*>(p) + i * B));
 #pragma unroll
-    for (int j = 0; j < B / 2; ++j) w[j] = at[j];
+    for (int j = 0; j < B / 2; ++j) w[j] = at[j].v;
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -90,6 +98,7 @@ struct Raw8 {
 };
 template <>
 struct Raw8<0> {
+  template <bool kLoose>
   __device__ __forceinline__ void load(const void*, int64_t) {}
   __device__ __forceinline__ void clear() {}
 };
@@ -120,7 +129,7 @@ __device__ __forceinline__ void widen(const Raw8<B> (&r)[V], int dt, float (&v)[
 // leave the normal numbers, the quotients themselves.  Adding 1.5 * 2^23 rounds
 // half to even and leaves the integer in the low byte; no |y / s| passes 127 by
 // more than a rounding.
-template <int V>
+template <bool kLoose, int V>
 __device__ __forceinline__ void put_codes(const float (&y)[V][8], float s, int8_t* q, int k, int step) {
   const float inv = 1.0f / s;
   constexpr float kMagic = 12582912.0f;
@@ -153,7 +162,12 @@ __device__ __forceinline__ void put_codes(const float (&y)[V][8], float s, int8_
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int at = i * step;
-    if (at < k) *gmem(reinterpret_cast<u32x2_t*>(q + at)) = c[i];
+    if (at + (kLoose ? 7 : 0) < k)
+      gmem(reinterpret_cast<Vec<u32x2_t, kLoose ? 1 : 8>*>(q + at))->v = c[i];
+    else if (kLoose && at < k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (at + 8 - k <= j) gmem(q + k - 8)[j] = static_cast<int8_t>(c[i][j >> 2] >> (8 * (j & 3)));
   }
 }
 
@@ -182,7 +196,71 @@ __device__ __forceinline__ float top_of(const float (&y)[V][8]) {
 // barrier).
 constexpr int row_block(int t) { return t == kWave ? 4 * t : t; }
 
-template <int XB, int RB, int T, int V>
+// kLoose: rows of any length from eight, at any address and stride.  The hardware takes
+// vector loads and stores at any address; a row's last run, where fewer than eight
+// values are left, is its last eight, of which those that the run before holds count
+// as zeros and are not stored (so that it does not matter whether the run before has
+// stored them, where r_out is r).  209 rows of 9213 values 5.8 us, 31 value by value;
+// 8192 of 2049 37.5, 110; 8192 of gate and up, 8191 each, 66, 264 (8192 each, aligned,
+// 60).
+template <bool kLoose, int V>
+__device__ __forceinline__ void drop_before(float (&h)[V][8], int c0, int step, int k) {
+  if constexpr (kLoose)
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = c0 + i * step + 8 - k <= j ? h[i][j] : 0.0f;
+}
+
+template <int DT>
+__device__ __forceinline__ void put(void* p, int64_t i, float v) {
+  if constexpr (DT == kActF32)
+    gmem(static_cast<float*>(p))[i] = v;
+  else
+    gmem(static_cast<uint16_t*>(p))[i] = static_cast<uint16_t>(pack2<DT>(v, 0.0f));
+}
+
+// eight values at any address
+template <int DT>
+__device__ __forceinline__ void put8(void* p, int64_t i, const float (&v)[8]) {
+  constexpr int B = DT == kActF32 ? 4 : 2;
+  SHERRY_GLOBAL Vec<u32x4_t, B>* to = gmem(reinterpret_cast<Vec<u32x4_t, B>*>(static_cast<char*>(p) + i * B));
+#pragma unroll
+  for (int h = 0; h < B / 2; ++h) {
+    u32x4_t w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = B == 4 ? __float_as_uint(v[4 * h + j]) : pack2<DT>(v[2 * j], v[2 * j + 1]);
+    to[h].v = w;
+  }
+}
+
+template <int RB, bool kLoose, int V>
+__device__ __forceinline__ void put_sum(const NormQuantArgs& a, int64_t row, int c0, int step, int rdt, const float (&h)[V][8]) {
+  const int k = static_cast<int>(a.k);
+  auto store = [&](auto dt) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = c0 + i * step;
+      if constexpr (!kLoose) {
+        if (c < k) store8<decltype(dt)::value>(a.r_out, row * a.ldro + c, h[i]);
+      } else if (c + 8 <= k) {
+        put8<decltype(dt)::value>(a.r_out, row * a.ldro + c, h[i]);
+      } else if (c < k) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + 8 - k <= j) put<decltype(dt)::value>(a.r_out, row * a.ldro + k - 8 + j, h[i][j]);
+      }
+    }
+  };
+  if constexpr (RB == 4)
+    store(std::integral_constant<int, kActF32>{});
+  else if (rdt == kActF16)
+    store(std::integral_constant<int, kActF16>{});
+  else
+    store(std::integral_constant<int, kActBf16>{});
+}
+
+template <int XB, int RB, bool kLoose, int T, int V>
 __global__ __launch_bounds__(row_block(T)) void rms_norm_quant_rows(NormQuantArgs a, int xdt, int rdt) {
   __shared__ double part[T / kWave];
   __shared__ float wmax[T / kWave];
@@ -195,9 +273,9 @@ __global__ __launch_bounds__(row_block(T)) void rms_norm_quant_rows(NormQuantArg
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = min(c0 + i * T * 8, k - 8);
-    x[i].load(a.x, row * a.ldx + c);
-    r[i].load(a.r, row * a.ldr + c);
-    w[i].load(a.w, c);
+    x[i].template load<kLoose>(a.x, row * a.ldx + c);
+    r[i].template load<kLoose>(a.r, row * a.ldr + c);
+    w[i].template load<kLoose>(a.w, c);
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {  // (runs past the row's end loaded its last, so that no load stands behind a branch)
@@ -214,20 +292,9 @@ __global__ __launch_bounds__(row_block(T)) void rms_norm_quant_rows(NormQuantArg
     for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[i][j] += g[i][j];
-    auto store = [&](auto dt) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = c0 + i * T * 8;
-        if (c < k) store8<decltype(dt)::value>(a.r_out, row * a.ldro + c, h[i]);
-      }
-    };
-    if constexpr (RB == 4)
-      store(std::integral_constant<int, kActF32>{});
-    else if (rdt == kActF16)
-      store(std::integral_constant<int, kActF16>{});
-    else
-      store(std::integral_constant<int, kActBf16>{});
+    put_sum<RB, kLoose, V>(a, row, c0, T * 8, rdt, h);
   }
+  drop_before<kLoose, V>(h, c0, T * 8, k);
   double ss = 0.0;
 #pragma unroll
   for (int i = 0; i < V; ++i)
@@ -241,7 +308,7 @@ __global__ __launch_bounds__(row_block(T)) void rms_norm_quant_rows(NormQuantArg
     for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * inv * __uint_as_float(w[i].w[j >> 2][j & 3]);
   const float s = act_scale(RowTeam<T>::max(top_of<V>(h), wmax));
   if ((threadIdx.x & (T - 1)) == 0) gmem(a.scales)[row] = s;
-  put_codes<V>(h, s, a.q + row * a.ldq + c0, k - c0, T * 8);
+  put_codes<kLoose, V>(h, s, a.q + row * a.ldq + c0, k - c0, T * 8);
 }
 
 // g / (1 + exp(-z)): SiLU with z = g, and GELU with z = 2 sqrt(2/pi) (g + 0.044715 g^3),
@@ -251,7 +318,22 @@ __device__ __forceinline__ float activate(float g, int act) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
 }
 
-template <int XB, int T, int V>
+// which activation it is, is the same for all of a launch
+template <int V>
+__device__ __forceinline__ void gate(float (&y)[V][8], const float (&v)[V][8], int act) {
+  auto each = [&](int act) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[i][j] = activate(y[i][j], act) * v[i][j];
+  };
+  if (act == kGateSilu)
+    each(kGateSilu);
+  else
+    each(kGateGeluTanh);
+}
+
+template <int XB, bool kLoose, int T, int V>
 __global__ __launch_bounds__(row_block(T)) void gated_quant_rows(GatedQuantArgs a, int dt) {
   __shared__ float wmax[T / kWave];
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (row_block(T) / T) + threadIdx.x / T;
@@ -261,8 +343,8 @@ __global__ __launch_bounds__(row_block(T)) void gated_quant_rows(GatedQuantArgs 
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = min(c0 + i * T * 8, k - 8);
-    g[i].load(a.gate, row * a.ldg + c);
-    u[i].load(a.up, row * a.ldu + c);
+    g[i].template load<kLoose>(a.gate, row * a.ldg + c);
+    u[i].template load<kLoose>(a.up, row * a.ldu + c);
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -273,76 +355,155 @@ __global__ __launch_bounds__(row_block(T)) void gated_quant_rows(GatedQuantArgs 
   float y[V][8], v[V][8];
   widen<XB, V>(g, dt, y);
   widen<XB, V>(u, dt, v);
-  auto each = [&](int act) {
+  gate<V>(y, v, a.act);
+  drop_before<kLoose, V>(y, c0, T * 8, k);
+  const float s = act_scale(RowTeam<T>::max(top_of<V>(y), wmax));
+  if ((threadIdx.x & (T - 1)) == 0) gmem(a.scales)[row] = s;
+  put_codes<kLoose, V>(y, s, a.q + row * a.ldq + c0, k - c0, T * 8);
+}
+
+// ---- rows that no workgroup's registers hold: the same runs, read again for each pass
+// (4096 rows of 40000 with an fp32 residual 525 us, 1460 where the passes went value by
+// value; 2048 of gate and up, 53248 each, 145 us, 493) ----
+
+constexpr int kLong = 1024;  // threads a row, of two runs at once
+
+template <int XB, int RB>
+__global__ __launch_bounds__(kLong) void rms_norm_quant_long(NormQuantArgs a, int xdt, int rdt) {
+  __shared__ double part[kLong / kWave];
+  __shared__ float wmax[kLong / kWave];
+  constexpr int V = 2, kStep = kLong * 8;
+  const int64_t row = blockIdx.x;
+  const int k = static_cast<int>(a.k), first = static_cast<int>(threadIdx.x) * 8;
+  auto values = [&](int c0, float (&h)[V][8]) {
+    Raw8<XB> x[V];
+    Raw8<RB> r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = min(c0 + i * kStep, k - 8);
+      x[i].template load<true>(a.x, row * a.ldx + c);
+      r[i].template load<true>(a.r, row * a.ldr + c);
+    }
+    widen<XB, V>(x, xdt, h);
+    if constexpr (RB > 0) {
+      float g[V][8];
+      widen<RB, V>(r, rdt, g);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] += g[i][j];
+    }
+    drop_before<true, V>(h, c0, kStep, k);
+  };
+  auto scaled = [&](int c0, float (&h)[V][8], float inv) {
+    Raw8<4> w[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i].template load<true>(a.w, min(c0 + i * kStep, k - 8));
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[i][j] = activate(y[i][j], act) * v[i][j];
+      for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * inv * __uint_as_float(w[i].w[j >> 2][j & 3]);
   };
-  if (a.act == kGateSilu)
-    each(kGateSilu);
-  else
-    each(kGateGeluTanh);
-  const float s = act_scale(RowTeam<T>::max(top_of<V>(y), wmax));
-  if ((threadIdx.x & (T - 1)) == 0) gmem(a.scales)[row] = s;
-  put_codes<V>(y, s, a.q + row * a.ldq + c0, k - c0, T * 8);
-}
-
-// ---- any row length, stride and alignment: one workgroup a row, value by value,
-// read again for each pass ----
-
-template <int DT>
-__device__ __forceinline__ void put(void* p, int64_t i, float v) {
-  if constexpr (DT == kActF32)
-    gmem(static_cast<float*>(p))[i] = v;
-  else
-    gmem(static_cast<uint16_t*>(p))[i] = static_cast<uint16_t>(pack2<DT>(v, 0.0f));
-}
-
-__global__ __launch_bounds__(kActThreads) void rms_norm_quant_any(NormQuantArgs a, int xdt, int rdt) {
-  __shared__ double part[kActThreads / kWave];
-  __shared__ float wmax[kActThreads / kWave];
-  const int64_t row = blockIdx.x;
-  auto value = [&](int64_t j) {
-    const float x = act_value(a.x, xdt, row * a.ldx + j);
-    return a.r ? x + act_value(a.r, rdt, row * a.ldr + j) : x;
-  };
+  float h[V][8];
   double ss = 0.0;
-  for (int64_t j = threadIdx.x; j < a.k; j += kActThreads) {
-    const double h = value(j);
-    ss = __builtin_fma(h, h, ss);
+  for (int c0 = first; c0 < k; c0 += V * kStep) {
+    values(c0, h);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = __builtin_fma(static_cast<double>(h[i][j]), static_cast<double>(h[i][j]), ss);
   }
-  ss = RowTeam<kActThreads>::sum(ss, part);
+  ss = RowTeam<kLong>::sum(ss, part);
   const float inv = norm_factor(ss, a);
   float amax = 0.0f;
-  for (int64_t j = threadIdx.x; j < a.k; j += kActThreads) amax = fmaxf(amax, fabsf(value(j) * inv * gmem(a.w)[j]));
-  const float s = act_scale(RowTeam<kActThreads>::max(amax, wmax));
+  for (int c0 = first; c0 < k; c0 += V * kStep) {
+    values(c0, h);
+    scaled(c0, h, inv);
+    amax = fmaxf(amax, top_of<V>(h));
+  }
+  const float s = act_scale(RowTeam<kLong>::max(amax, wmax));
   if (threadIdx.x == 0) gmem(a.scales)[row] = s;
-  // (a thread reads r where it writes r_out, which may be the same memory)
-  for (int64_t j = threadIdx.x; j < a.k; j += kActThreads) {
-    const float h = value(j);
-    gmem(a.q)[row * a.ldq + j] = act_code(h * inv * gmem(a.w)[j], s);
-    if (!a.r) continue;
-    if (rdt == kActF32)
-      put<kActF32>(a.r_out, row * a.ldro + j, h);
-    else if (rdt == kActF16)
-      put<kActF16>(a.r_out, row * a.ldro + j, h);
-    else
-      put<kActBf16>(a.r_out, row * a.ldro + j, h);
+  // (a thread reads the values of r that count for it where it writes r_out, which may
+  // be the same memory)
+  for (int c0 = first; c0 < k; c0 += V * kStep) {
+    values(c0, h);
+    if constexpr (RB > 0) put_sum<RB, true, V>(a, row, c0, kStep, rdt, h);
+    scaled(c0, h, inv);
+    put_codes<true, V>(h, s, a.q + row * a.ldq + c0, k - c0, kStep);
   }
 }
 
-__global__ __launch_bounds__(kActThreads) void gated_quant_any(GatedQuantArgs a, int dt) {
-  __shared__ float wmax[kActThreads / kWave];
+template <int XB>
+__global__ __launch_bounds__(kLong) void gated_quant_long(GatedQuantArgs a, int dt) {
+  __shared__ float wmax[kLong / kWave];
+  constexpr int V = 2, kStep = kLong * 8;
   const int64_t row = blockIdx.x;
-  auto value = [&](int64_t j) {
-    return activate(act_value(a.gate, dt, row * a.ldg + j), a.act) * act_value(a.up, dt, row * a.ldu + j);
+  const int k = static_cast<int>(a.k), first = static_cast<int>(threadIdx.x) * 8;
+  auto values = [&](int c0, float (&y)[V][8]) {
+    Raw8<XB> g[V], u[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = min(c0 + i * kStep, k - 8);
+      g[i].template load<true>(a.gate, row * a.ldg + c);
+      u[i].template load<true>(a.up, row * a.ldu + c);
+    }
+    float v[V][8];
+    widen<XB, V>(g, dt, y);
+    widen<XB, V>(u, dt, v);
+    gate<V>(y, v, a.act);
+    drop_before<true, V>(y, c0, kStep, k);
   };
-  float amax = 0.0f;
-  for (int64_t j = threadIdx.x; j < a.k; j += kActThreads) amax = fmaxf(amax, fabsf(value(j)));
-  const float s = act_scale(RowTeam<kActThreads>::max(amax, wmax));
+  float y[V][8], amax = 0.0f;
+  for (int c0 = first; c0 < k; c0 += V * kStep) {
+    values(c0, y);
+    amax = fmaxf(amax, top_of<V>(y));
+  }
+  const float s = act_scale(RowTeam<kLong>::max(amax, wmax));
   if (threadIdx.x == 0) gmem(a.scales)[row] = s;
-  for (int64_t j = threadIdx.x; j < a.k; j += kActThreads) gmem(a.q)[row * a.ldq + j] = act_code(value(j), s);
+  for (int c0 = first; c0 < k; c0 += V * kStep) {
+    values(c0, y);
+    put_codes<true, V>(y, s, a.q + row * a.ldq + c0, k - c0, kStep);
+  }
+}
+
+// ---- rows of fewer than eight values: a wave a row, a value a lane ----
+
+__global__ __launch_bounds__(row_block(kWave)) void rms_norm_quant_short(NormQuantArgs a, int xdt, int rdt) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (row_block(kWave) / kWave) + threadIdx.x / kWave;
+  if (row >= a.m) return;
+  const int j = static_cast<int>(threadIdx.x & (kWave - 1));
+  const bool in = j < a.k;
+  float h = 0.0f, w = 0.0f;
+  if (in) {
+    h = act_value(a.x, xdt, row * a.ldx + j);
+    w = gmem(a.w)[j];
+    if (a.r) h += act_value(a.r, rdt, row * a.ldr + j);
+  }
+  const double ss = RowTeam<kWave>::sum(static_cast<double>(h) * h, nullptr);
+  const float y = h * norm_factor(ss, a) * w;
+  const float s = act_scale(RowTeam<kWave>::max(fabsf(y), nullptr));
+  if (j == 0) gmem(a.scales)[row] = s;
+  if (!in) return;
+  gmem(a.q)[row * a.ldq + j] = act_code(y, s);
+  if (!a.r) return;
+  if (rdt == kActF32)
+    put<kActF32>(a.r_out, row * a.ldro + j, h);
+  else if (rdt == kActF16)
+    put<kActF16>(a.r_out, row * a.ldro + j, h);
+  else
+    put<kActBf16>(a.r_out, row * a.ldro + j, h);
+}
+
+__global__ __launch_bounds__(row_block(kWave)) void gated_quant_short(GatedQuantArgs a, int dt) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (row_block(kWave) / kWave) + threadIdx.x / kWave;
+  if (row >= a.m) return;
+  const int j = static_cast<int>(threadIdx.x & (kWave - 1));
+  const bool in = j < a.k;
+  float y = 0.0f;
+  if (in) y = activate(act_value(a.gate, dt, row * a.ldg + j), a.act) * act_value(a.up, dt, row * a.ldu + j);
+  const float s = act_scale(RowTeam<kWave>::max(fabsf(y), nullptr));
+  if (j == 0) gmem(a.scales)[row] = s;
+  if (in) gmem(a.q)[row * a.ldq + j] = act_code(y, s);
 }
 
 // ---- which threads a row gets ----
@@ -391,12 +552,32 @@ dim3 row_grid(int64_t m) {
   return dim3(static_cast<unsigned>((m + rows - 1) / rows));
 }
 
-template <int XB, int RB>
-bool launch_norm_rows(const NormQuantArgs& a, int xdt, int rdt, hipStream_t stream) {
-  return row_shape<true>(a.k, [&](auto t, auto v) {
+template <int XB, int RB, bool kLoose>
+void launch_norm_rows(const NormQuantArgs& a, int xdt, int rdt, hipStream_t stream) {
+  const bool done = row_shape<true>(a.k, [&](auto t, auto v) {
     constexpr int T = decltype(t)::value, V = decltype(v)::value;
-    hipLaunchKernelGGL((rms_norm_quant_rows<XB, RB, T, V>), row_grid<T>(a.m), dim3(row_block(T)), 0, stream, a, xdt, rdt);
+    hipLaunchKernelGGL((rms_norm_quant_rows<XB, RB, kLoose, T, V>), row_grid<T>(a.m), dim3(row_block(T)), 0, stream, a, xdt,
+                       rdt);
   });
+  if (!done) hipLaunchKernelGGL((rms_norm_quant_long<XB, RB>), dim3(static_cast<unsigned>(a.m)), dim3(kLong), 0, stream, a, xdt, rdt);
+}
+
+template <bool kLoose>
+void launch_norm(const NormQuantArgs& a, int xdt, int rdt, int64_t xb, int64_t rb, hipStream_t stream) {
+  if (xb == 2)
+    return rb == 0 ? launch_norm_rows<2, 0, kLoose>(a, xdt, rdt, stream)
+           : rb == 2 ? launch_norm_rows<2, 2, kLoose>(a, xdt, rdt, stream) : launch_norm_rows<2, 4, kLoose>(a, xdt, rdt, stream);
+  return rb == 0 ? launch_norm_rows<4, 0, kLoose>(a, xdt, rdt, stream)
+         : rb == 2 ? launch_norm_rows<4, 2, kLoose>(a, xdt, rdt, stream) : launch_norm_rows<4, 4, kLoose>(a, xdt, rdt, stream);
+}
+
+template <int XB, bool kLoose>
+void launch_gated(const GatedQuantArgs& a, int dt, hipStream_t stream) {
+  const bool done = row_shape<false>(a.k, [&](auto t, auto v) {
+    constexpr int T = decltype(t)::value, V = decltype(v)::value;
+    hipLaunchKernelGGL((gated_quant_rows<XB, kLoose, T, V>), row_grid<T>(a.m), dim3(row_block(T)), 0, stream, a, dt);
+  });
+  if (!done) hipLaunchKernelGGL((gated_quant_long<XB>), dim3(static_cast<unsigned>(a.m)), dim3(kLong), 0, stream, a, dt);
 }
 
 }  // namespace
@@ -405,34 +586,24 @@ hipError_t launch_rms_norm_quant(const NormQuantArgs& a, int xdt, int rdt, hipSt
   const int64_t xb = act_bytes(xdt), rb = a.r ? act_bytes(rdt) : 0;
   const bool runs = a.k % 8 == 0 && row_runs(a.x, a.ldx, xb) && row_runs(a.q, a.ldq, 1) && row_runs(a.w, 8, 4) &&
                     (!a.r || (row_runs(a.r, a.ldr, rb) && row_runs(a.r_out, a.ldro, rb)));
-  bool done = false;
-  if (runs) {
-    if (xb == 2)
-      done = rb == 0 ? launch_norm_rows<2, 0>(a, xdt, rdt, stream)
-             : rb == 2 ? launch_norm_rows<2, 2>(a, xdt, rdt, stream) : launch_norm_rows<2, 4>(a, xdt, rdt, stream);
-    else
-      done = rb == 0 ? launch_norm_rows<4, 0>(a, xdt, rdt, stream)
-             : rb == 2 ? launch_norm_rows<4, 2>(a, xdt, rdt, stream) : launch_norm_rows<4, 4>(a, xdt, rdt, stream);
-  }
-  if (!done)
-    hipLaunchKernelGGL(rms_norm_quant_any, dim3(static_cast<unsigned>(a.m)), dim3(kActThreads), 0, stream, a, xdt, rdt);
+  if (a.k < 8)
+    hipLaunchKernelGGL(rms_norm_quant_short, row_grid<kWave>(a.m), dim3(row_block(kWave)), 0, stream, a, xdt, rdt);
+  else if (runs)
+    launch_norm<false>(a, xdt, rdt, xb, rb, stream);
+  else
+    launch_norm<true>(a, xdt, rdt, xb, rb, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_gated_quant(const GatedQuantArgs& a, int dt, hipStream_t stream) {
   const int64_t b = act_bytes(dt);
-  auto rows = [&](auto bytes) {
-    return row_shape<false>(a.k, [&](auto t, auto v) {
-      constexpr int T = decltype(t)::value, V = decltype(v)::value;
-      hipLaunchKernelGGL((gated_quant_rows<decltype(bytes)::value, T, V>), row_grid<T>(a.m), dim3(row_block(T)), 0, stream,
-                         a, dt);
-    });
-  };
-  bool done = false;
-  if (a.k % 8 == 0 && row_runs(a.gate, a.ldg, b) && row_runs(a.up, a.ldu, b) && row_runs(a.q, a.ldq, 1))
-    done = b == 2 ? rows(std::integral_constant<int, 2>{}) : rows(std::integral_constant<int, 4>{});
-  if (!done)
-    hipLaunchKernelGGL(gated_quant_any, dim3(static_cast<unsigned>(a.m)), dim3(kActThreads), 0, stream, a, dt);
+  const bool runs = a.k % 8 == 0 && row_runs(a.gate, a.ldg, b) && row_runs(a.up, a.ldu, b) && row_runs(a.q, a.ldq, 1);
+  if (a.k < 8)
+    hipLaunchKernelGGL(gated_quant_short, row_grid<kWave>(a.m), dim3(row_block(kWave)), 0, stream, a, dt);
+  else if (b == 2)
+    runs ? launch_gated<2, false>(a, dt, stream) : launch_gated<2, true>(a, dt, stream);
+  else
+    runs ? launch_gated<4, false>(a, dt, stream) : launch_gated<4, true>(a, dt, stream);
   return hipGetLastError();
 }
 
