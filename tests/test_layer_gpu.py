@@ -891,3 +891,13 @@ def test_gated_any_place(gpu_lib, k, dtype, first):
     q2, s2 = gpu_lib.gated_quant(g.contiguous(), u.contiguous())
     assert torch.equal(q, q2) and torch.equal(s, s2)
     assert (q_wide[:, :first] == 77).all() and (q_wide[:, first + k:] == 77).all()
+
+
+@pytest.mark.parametrize("k", [1032, 1536, 2072, 3064, 4104, 6144, 6152, 12288, 12296, 24576, 24584])
+@pytest.mark.parametrize("m", [1, 300])
+def test_rows_aligned_shapes(gpu_lib, k, m):
+    """Aligned rows on both sides of where a row gets more threads."""
+    say("rows aligned shapes", k, m)
+    check_norm(gpu_lib, *norm_inputs(m, k, torch.bfloat16, torch.float16, 1500 + k))
+    gu = randn(m, 2 * k, seed=1600 + k).half().to(DEV)
+    check_gated(gpu_lib, gu[:, :k], gu[:, k:], "gelu_tanh")

@@ -200,8 +200,8 @@ constexpr int row_block(int t) { return t == kWave ? 4 * t : t; }
 // vector loads and stores at any address; a row's last run, where fewer than eight
 // values are left, is its last eight, of which those that the run before holds count
 // as zeros and are not stored (so that it does not matter whether the run before has
-// stored them, where r_out is r).  209 rows of 9213 values 5.8 us, 31 value by value;
-// 8192 of 2049 37.5, 110; 8192 of gate and up, 8191 each, 66, 264 (8192 each, aligned,
+// stored them, where r_out is r).  209 rows of 9213 values 5.2 us, 31 value by value;
+// 8192 of 2049 34.6, 110; 8192 of gate and up, 8191 each, 66, 264 (8192 each, aligned,
 // 60).
 template <bool kLoose, int V>
 __device__ __forceinline__ void drop_before(float (&h)[V][8], int c0, int step, int k) {
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(row_block(T)) void rms_norm_quant_rows(NormQuantArg
   __shared__ float wmax[T / kWave];
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (row_block(T) / T) + threadIdx.x / T;
   if (row >= a.m) return;  // (whole waves, and only where a row is one)
-  const int k = static_cast<int>(a.k), c0 = static_cast<int>(threadIdx.x & (T - 1)) * 8;
+  const int k = static_cast<int>(a.k), c0 = static_cast<int>(threadIdx.x % T) * 8;
   Raw8<XB> x[V];
   Raw8<RB> r[V];
   Raw8<4> w[V];
@@ -307,7 +307,7 @@ __global__ __launch_bounds__(row_block(T)) void rms_norm_quant_rows(NormQuantArg
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * inv * __uint_as_float(w[i].w[j >> 2][j & 3]);
   const float s = act_scale(RowTeam<T>::max(top_of<V>(h), wmax));
-  if ((threadIdx.x & (T - 1)) == 0) gmem(a.scales)[row] = s;
+  if (c0 == 0) gmem(a.scales)[row] = s;
   put_codes<kLoose, V>(h, s, a.q + row * a.ldq + c0, k - c0, T * 8);
 }
 
@@ -338,7 +338,7 @@ __global__ __launch_bounds__(row_block(T)) void gated_quant_rows(GatedQuantArgs 
   __shared__ float wmax[T / kWave];
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (row_block(T) / T) + threadIdx.x / T;
   if (row >= a.m) return;
-  const int k = static_cast<int>(a.k), c0 = static_cast<int>(threadIdx.x & (T - 1)) * 8;
+  const int k = static_cast<int>(a.k), c0 = static_cast<int>(threadIdx.x % T) * 8;
   Raw8<XB> g[V], u[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -358,7 +358,7 @@ __global__ __launch_bounds__(row_block(T)) void gated_quant_rows(GatedQuantArgs 
   gate<V>(y, v, a.act);
   drop_before<kLoose, V>(y, c0, T * 8, k);
   const float s = act_scale(RowTeam<T>::max(top_of<V>(y), wmax));
-  if ((threadIdx.x & (T - 1)) == 0) gmem(a.scales)[row] = s;
+  if (c0 == 0) gmem(a.scales)[row] = s;
   put_codes<kLoose, V>(y, s, a.q + row * a.ldq + c0, k - c0, T * 8);
 }
 
@@ -523,6 +523,10 @@ bool row_runs(const void* p, int64_t ld, int64_t bytes) {
 //                      registers leave room for one row more a CU; 93.5 with one),
 //                      85.3 / 63.5
 //   4096 of 16384:     105 / 65.5, 88.3 / 61.0
+// The threads go up by a half and a third, since waves without values take a row's
+// place on a CU all the same: by doublings alone 8192 rows of 1280 took 17.0 / 14.1 (now
+// 14.7 / 12.0), of 2560 34.5 / 25.8 (30.7 / 23.7), 4096 of gate and up, 18944 each,
+// 108 (91).
 template <bool kNorm, class F>
 bool row_shape(int64_t k, F f) {
   auto go = [&](auto t, auto v) {
@@ -533,14 +537,19 @@ bool row_shape(int64_t k, F f) {
   if (k <= (T) * (V) * 8) return go(std::integral_constant<int, T>{}, std::integral_constant<int, V>{})
   SHERRY_ROW(64, 1);
   SHERRY_ROW(128, 1);
+  SHERRY_ROW(192, 1);
   SHERRY_ROW(256, 1);
+  SHERRY_ROW(384, 1);
   SHERRY_ROW(512, 1);
   if constexpr (kNorm) {
     SHERRY_ROW(512, 2);
   } else {
+    SHERRY_ROW(768, 1);
     SHERRY_ROW(1024, 1);
   }
+  SHERRY_ROW(768, 2);
   SHERRY_ROW(1024, 2);
+  SHERRY_ROW(768, 4);
   SHERRY_ROW(1024, 4);
 #undef SHERRY_ROW
   return false;
