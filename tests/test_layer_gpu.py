@@ -901,3 +901,37 @@ def test_rows_aligned_shapes(gpu_lib, k, m):
     check_norm(gpu_lib, *norm_inputs(m, k, torch.bfloat16, torch.float16, 1500 + k))
     gu = randn(m, 2 * k, seed=1600 + k).half().to(DEV)
     check_gated(gpu_lib, gu[:, :k], gu[:, k:], "gelu_tanh")
+
+
+@pytest.mark.parametrize("hq,hkv,d,n,length", [(32, 8, 64, 1100, 2700), (8, 2, 64, 60, 4500), (8, 2, 128, 40, 4500),
+                                               (6, 2, 128, 40, 2200)])
+def test_window_many_pages(gpu_lib, hq, hkv, d, n, length):
+    """Many rows over more blocks than page numbers are held at a time, in one split."""
+    say("window many pages", hq, hkv, d, n, length)
+    b = WindowBatch(gpu_lib, [n], [length], hq, hkv, d, 32, torch.bfloat16, 800 + d, length - n - 70, 40)
+    b.check(*b.run(max_kv=100))
+
+
+@pytest.mark.parametrize("hq,hkv,d,n,length", [(32, 8, 64, 1100, 1400), (8, 2, 64, 70, 200), (8, 2, 128, 70, 200)])
+@pytest.mark.parametrize("power", [20, 26, 40])
+def test_window_many_rows_huge_scores(gpu_lib, hq, hkv, d, n, length, power):
+    """Scores that fp32 has only to units and more: every row keeps a sum and finite
+    values between the least and the largest of V; rows of ordinary size among them
+    stay within their bound."""
+    say("window huge scores", hq, hkv, d, n, length, power)
+    b = WindowBatch(gpu_lib, [n], [length], hq, hkv, d, 32, torch.bfloat16, 820 + d, 100, 4)
+    o, lse = b.run()
+    b.check(o, lse)
+    sound = b.q.clone()
+    big = torch.arange(n, device=b.q.device) % 5 == 2
+    b.q[big] *= 2.0 ** power
+    o2, lse2 = b.run()
+    torch.cuda.synchronize()
+    gpu_big = big.to(o2.device)
+    assert torch.isfinite(o2).all() and torch.isfinite(lse2).all()
+    vd, vround, _ = b.vd[0]
+    top = float(np.abs(vd).max() + np.abs(vround).max()) * (1 + 2.0 ** -7)
+    assert o2[gpu_big].abs().max().item() <= top
+    b.q = sound
+    o2[gpu_big], lse2[gpu_big] = o[gpu_big], lse[gpu_big]
+    b.check(o2, lse2)
