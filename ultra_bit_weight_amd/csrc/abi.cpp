@@ -568,7 +568,7 @@ sherry_status attn_sizes(const sherry_kv4_cache* cache, int64_t n_tokens, int32_
   a->row_tiles = static_cast<int32_t>(tiles);
   const int64_t tile_tokens = std::min<int64_t>(max_q, (a->tile_rows + a->group - 1) / a->group);
   const int64_t seen = std::min(w.tokens, kMaxKv) + std::min(w.sinks, kMaxKv) + tile_tokens;
-  a->splits = w.on ? kv4_attn_window_splits(a->tile_rows, tiles * heads, std::min(max_kv, seen))
+  a->splits = w.on ? kv4_attn_window_splits(a->tile_rows, tiles * heads, std::min(max_kv, seen), cache->head_dim)
                    : kv4_attn_splits(a->tile_rows, tiles * heads, max_kv);
   *workspace = a->splits == 1 ? 0 : static_cast<size_t>(a->splits) * n_tokens * n_q_heads * (cache->head_dim + 2) * 4;
   return SHERRY_OK;

@@ -43,6 +43,7 @@
 // an exponent in fp16 as in bf16 (a shift and one mask-and-or), with 16 s taken
 // off z.  The powers of two are taken off the scores and off O.
 #include <algorithm>
+#include <limits>
 #include <type_traits>
 
 #include "kv4.h"
@@ -1172,6 +1173,14 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
   if (a.splits > 1) {
     int sg = 0;
     while (sg < (D == 64 ? 4 : 3) && (2 << sg) <= a.splits) ++sg;
+    // With a window groups of four splits each, since what those that are not there
+    // load (the first again) counts where rows are many.  (Two groups at D = 64 are
+    // slower than one or four: 37.2 against 32.2 us for 512 tokens in six splits.)
+    if constexpr (kWin) {
+      sg = 0;
+      while (sg < (D == 64 ? 4 : 3) && 4 << sg < a.splits) ++sg;
+      if (D == 64 && sg == 1) sg = 2;
+    }
     const int rows_per = kAttnThreads / (D / 4) >> sg;
     const int64_t jb = (static_cast<int64_t>(a.max_q) * a.n_q_heads + rows_per - 1) / rows_per;
     hipLaunchKernelGGL((kv4_join_kernel<D, DT>), dim3(static_cast<unsigned>(jb * a.n_seqs)), block, 0, stream, a,
@@ -1254,11 +1263,33 @@ int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim) {
 }
 
 // Windows are as long as one another, so there is nothing to even out where the
-// workgroups fill the chip, and a join to save: few rows from one workgroup a CU on
-// (48 tokens, window 2048, D = 128: 29.0 us, 33.6 in two; 128, window 4096, D = 64:
-// 58.3, 63.1), more from two (512 tokens, window 1000: 31.5 with 256, 28.7 split).
-int32_t kv4_attn_window_splits(int32_t tile_rows, int64_t workgroups, int64_t max_seen) {
-  return workgroups >= (tile_rows <= 16 ? 256 : 512) ? 1 : kv4_attn_splits(tile_rows, workgroups, max_seen);
+// workgroups fill the chip, and a join to save: few rows are not split from one
+// workgroup a CU on (48 tokens, window 2048, D = 128: 29.0 us, 33.6 in two; 128, window
+// 4096, D = 64: 58.3, 63.1), more from two.  Below that, the number of splits with the
+// least time by what was measured of many rows: a step of a block takes longer the more
+// workgroups a CU has (D = 64: 0.75, 0.9, 1.05, 1.2 us with one to four, which is what
+// the registers hold; eight waves, two; D = 128, three), and a join 3.5 us and what its
+// shares take to write and read.  Of 31 cases (32 to 1000 tokens, windows of 256 to
+// 4096, 16 to 376 workgroups, 1 to 16 splits) that is the best in 26 and 1.007 of it in
+// the mean; us here / as without a window: 512 tokens, D = 64, windows of 1000 and
+// 4096 26.8 / 26.9 and 52.2 / 64.1; 256, 4096 32.5 / 38.9; 1000, 1000 28.0 / 35.0;
+// D = 128, 512 tokens, 256 and 4096 16.4 / 22.2 and 66.4 / 79.7.
+int32_t kv4_attn_window_splits(int32_t tile_rows, int64_t workgroups, int64_t max_seen, int head_dim) {
+  const bool few = tile_rows <= 16;
+  if (workgroups >= (few ? 256 : 512)) return 1;
+  if (few) return kv4_attn_splits(tile_rows, workgroups, max_seen);
+  const bool eight = tile_rows == 32 * kAttnWaves;
+  const int64_t fit = eight ? 512 : head_dim == 64 ? 1024 : 768;
+  const int64_t first = head_dim == 64 && !eight ? 600 : 400, more = eight ? 200 : head_dim == 64 ? 150 : 250;  // ns
+  const int64_t blocks = max_seen / kKv4Block + 2;
+  int64_t best = 1, least = std::numeric_limits<int64_t>::max();
+  for (int64_t n = 1; n == 1 || (n * workgroups <= fit && 2 * n <= blocks); n += 1 + n / 16) {
+    const int64_t total = n * workgroups;
+    const int64_t time = (blocks + n - 1) / n * (first + more * ((total + 255) / 256)) +
+                         (n == 1 ? 0 : 3500 + total * tile_rows * head_dim / 800);
+    if (time < least) best = n, least = time;
+  }
+  return static_cast<int32_t>(best);
 }
 
 hipError_t launch_kv4_attn(const AttnArgs& a, int head_dim, int dt, hipStream_t stream) {
