@@ -561,14 +561,15 @@ sherry_status attn_sizes(const sherry_kv4_cache* cache, int64_t n_tokens, int32_
   if (rows > kMaxDim / 256) return SHERRY_ESHAPE;
   const int64_t heads = static_cast<int64_t>(n_seqs) * a->c.n_kv_heads;
   max_kv = std::min(max_kv, kMaxKv);
-  a->tile_rows = w.on ? kv4_attn_window_tile_rows(rows, heads, cache->head_dim)
+  const int64_t window = std::min(w.tokens, kMaxKv) + std::min(w.sinks, kMaxKv);
+  a->tile_rows = w.on ? kv4_attn_window_tile_rows(rows, heads, cache->head_dim, std::min(max_kv, window))
                       : kv4_attn_tile_rows(rows, heads, cache->head_dim, max_q, max_kv);
   const int64_t tiles = (rows + a->tile_rows - 1) / a->tile_rows;
   if (tiles > kMaxDim / (w.on ? 512 : 256) / heads) return SHERRY_ESHAPE;  // threads of the launch
   a->row_tiles = static_cast<int32_t>(tiles);
   const int64_t tile_tokens = std::min<int64_t>(max_q, (a->tile_rows + a->group - 1) / a->group);
-  const int64_t seen = std::min(w.tokens, kMaxKv) + std::min(w.sinks, kMaxKv) + tile_tokens;
-  a->splits = w.on ? kv4_attn_window_splits(a->tile_rows, tiles * heads, std::min(max_kv, seen), cache->head_dim)
+  a->splits = w.on ? kv4_attn_window_splits(a->tile_rows, tiles * heads, std::min(max_kv, window + tile_tokens),
+                                            cache->head_dim)
                    : kv4_attn_splits(a->tile_rows, tiles * heads, max_kv);
   *workspace = a->splits == 1 ? 0 : static_cast<size_t>(a->splits) * n_tokens * n_q_heads * (cache->head_dim + 2) * 4;
   return SHERRY_OK;

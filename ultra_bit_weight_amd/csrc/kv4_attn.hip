@@ -1253,13 +1253,29 @@ int32_t kv4_attn_splits(int32_t tile_rows, int64_t workgroups, int64_t max_kv) {
   return static_cast<int32_t>(n);
 }
 
-// With a window, many rows: eight waves a workgroup where the registers allow it
-// (D = 64) and that leaves a workgroup a CU (512 tokens over 2048, window 256: 18.5
-// us with eight, 12.6 with four).
-int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim) {
+// With a window the kernel that shares out the tokens takes more rows too, 16 a
+// workgroup, where those are so few, or see so little, that what counts is how soon
+// each is through, not that every 16 rows unpack their tokens for themselves.  Beyond,
+// eight waves a workgroup where the registers allow it (D = 64) and that leaves a
+// workgroup a CU (512 tokens over 2048, window 256: 18.5 us with eight, 12.6 with four).
+// us, shared out / by rows, workgroups of 16 rows in brackets, windows of 100, 500, 2000
+// and 6000:
+//   D = 64, 32 rows [16]     5.4 / 8.5, 6.9 / 9.1, 7.9 / 10.4, 9.1 / 12.9
+//           32 rows [1024]   8.3 / 10.6, 13.4 / 18.2, 34.4 / 46.9, 86 / 123
+//           64 rows [768]    7.4 / 8.9, 11.6 / 20.7, 26.1 / 30.6, 65 / 56
+//           64 rows [2048]   13.8 / 11.0, 23.4 / 20.2, 62.9 / 48.2
+//           256 rows [128]   5.8 / 9.6, 7.3 / 10.9, 11.9 / 13.6, 18.7 / 25.6
+//           384 rows [192]   5.8 / 9.6, 7.4 / 11.4, 15.6 / 15.6, 27.0 / 22.7
+//   D = 128, 48 rows [24]    7.0 / 10.1, 9.6 / 10.8, 11.7 / 13.2, 15.2 / 17.0
+//           126 rows [384]   8.9 / 12.0, 13.7 / 19.7, 29.1 / 32.4, 72 / 52
+//           63 rows [768]    13.1 / 10.8, 18.8 / 23.2, 44.6 / 41.5
+int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t seen) {
   if (rows <= 16) return rows <= 8 ? 8 : 16;
+  const int64_t few = (rows + 15) / 16 * heads;
+  const bool wide = head_dim == 128;
+  if ((rows <= 32 && !wide) || few <= (wide ? 64 : 128) || (few <= (wide ? 400 : 800) && seen <= 2200)) return 16;
   constexpr int32_t one = 16 * kAttnWaves;
-  return head_dim == 128 || (rows + 2 * one - 1) / (2 * one) * heads < 256 ? one : 2 * one;
+  return wide || (rows + 2 * one - 1) / (2 * one) * heads < 256 ? one : 2 * one;
 }
 
 // Windows are as long as one another, so there is nothing to even out where the

@@ -358,7 +358,7 @@ struct AttnArgs {
 // shares that a sequence's cached tokens are split into; and the same with a window
 // (max_seen: what the rows of a workgroup see together).
 int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv);
-int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim);
+int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t seen);
 int32_t kv4_attn_window_splits(int32_t tile_rows, int64_t workgroups, int64_t max_seen, int head_dim);
 int32_t kv4_attn_splits(int32_t tile_rows, int64_t workgroups, int64_t max_kv);
 hipError_t launch_kv4_attn(const AttnArgs& a, int head_dim, int dt, hipStream_t stream);
