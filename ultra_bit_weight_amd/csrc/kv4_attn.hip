@@ -901,10 +901,12 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
 // the blocks at either end of a tile's window, whose scores are tested one by one.
 // 2048 tokens of 32 heads on 8 over 8192, D = 64, us, with one / two / four tiles
 // on four waves, and with eight waves: window 1000 48.1 / 47.7 / 63.0, 42.9; 4096
-// 158 / 155 / 144, 137; and with the softmax's wave priority 41.9 and 130 (530
-// Tflop/s).  D = 128, five prompts of up to 1777 with a window of 512: 87.2 / 94.2;
-// eight waves 95.6, their registers spilled; with the priority 91.7 (though 187 for 201
-// with a window of 4096).
+// 158 / 155 / 144, 137; and with the softmax's wave priority 41.9 and 130, with page
+// numbers of 64 blocks at once 39.9 and 123, with the maximum folded 39.5 and 118 (590
+// Tflop/s); sixteen waves 40.1 and 119.  D = 128, five prompts of up to 1777 with a
+// window of 512: 87.2 / 94.2; eight waves 95.6, their registers spilled; with
+// page numbers of 64 blocks 85.3; with the priority 1 % more, but 2048 tokens over 8192,
+// windows of 512, 1000 and 4096, 37.6, 58.4, 196 -> 35.7, 55.7, 185.
 template <int D, int DT, int W>
 __global__ __launch_bounds__(W * kWave, W == 8 ? 4 : D == 128 ? 3 : 2) void kv4_attn_window_rows_kernel(AttnArgs a) {
   using L = Kv4Layout<D>;
@@ -1028,7 +1030,7 @@ __global__ __launch_bounds__(W * kWave, W == 8 ? 4 : D == 128 ? 3 : 2) void kv4_
   }
 
   auto block_step = [&](const RowsBuf<D>& from, int t_blk, auto edge) {
-    constexpr bool kFirst = D == 64 && !edge.value;
+    constexpr bool kFirst = !edge.value;
     f32x4_t c[2][NG];
 #pragma unroll
     for (int i = 0; i < NG; ++i)
