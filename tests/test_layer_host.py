@@ -200,3 +200,20 @@ def test_binding_refuses_window(lib):  # noqa: F811
     for bad in (dict(window=1.5), dict(window="4"), dict(window=4, sinks=None), dict(window=4, sinks=0.5)):
         with pytest.raises(TypeError):
             sherry.kv4_attn(c, **base, **bad)
+
+
+@pytest.mark.parametrize("hkv,group,d,seqs,q", [(8, 8, 64, 6, 13), (2, 8, 128, 8, 53), (1, 4, 64, 22, 25), (2, 2, 128, 49, 25),
+                                                (16, 2, 128, 2, 29), (3, 1, 64, 2, 705), (2, 3, 64, 2, 221), (1, 16, 64, 15, 62),
+                                                (1, 1, 128, 3, 725), (8, 4, 64, 1, 512), (8, 3, 128, 1, 512), (1, 1, 64, 1, 33)])
+def test_window_workspace_grows_with_max_kv(lib, hkv, group, d, seqs, q):  # noqa: F811
+    """What is asked for at one max_kv serves every smaller one, also where that takes
+    other tiles; the default serves all."""
+    c = sherry.Kv4Cache(4, 64, hkv, d, device="cpu")
+    f = lib.sherry_kv4_attn_window_workspace
+    for w, sinks in ((7, 3000), (83, 3000), (201, 3000), (518, 100), (757, 4), (2256, 0), (4074, 4), (9000, 50)):
+        needs = [f(c.desc, seqs * q, hkv * group, seqs, q, kv, w, sinks)
+                 for kv in [*range(1, 2199, 13), 2199, 2200, 2201, *range(2500, 9200, 97), 1 << 20, 1 << 30]]
+        for kv, a, b in zip(range(len(needs)), needs, needs[1:]):
+            assert a <= b, (w, sinks, kv, a, b)
+        assert needs[-1] <= min(sherry.kv4_attn_workspace(c, seqs * q, hkv * group, seqs, q, window=w, sinks=sinks).numel(),
+                                sherry.KV4_ATTN_WORKSPACE_MAX)

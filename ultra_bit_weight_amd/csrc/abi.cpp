@@ -930,6 +930,12 @@ size_t sherry_kv4_attn_window_workspace(const sherry_kv4_cache* cache, int64_t n
   if (n_tokens <= 0 || n_seqs <= 0 || check_cache(cache, &a.c) != SHERRY_OK) return 0;
   if (attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, max_kv, Window{true, window, sinks}, &a, &need) != SHERRY_OK)
     return 0;
+  // (shorter sequences may take smaller tiles)
+  size_t few = 0;
+  if (attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, std::min(max_kv, kWindowShort), Window{true, window, sinks}, &a,
+                 &few) != SHERRY_OK)
+    return 0;
+  need = std::max(need, few);
   // (the table may turn out to hold no more than the window)
   size_t none = 0;
   if (attn_sizes(cache, n_tokens, n_q_heads, n_seqs, max_q, std::min(max_kv, window), Window{}, &a, &none) != SHERRY_OK)

@@ -43,7 +43,6 @@
 // an exponent in fp16 as in bf16 (a shift and one mask-and-or), with 16 s taken
 // off z.  The powers of two are taken off the scores and off O.
 #include <algorithm>
-#include <limits>
 #include <type_traits>
 
 #include "kv4.h"
@@ -1275,7 +1274,7 @@ int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim, int
   if (rows <= 16) return rows <= 8 ? 8 : 16;
   const int64_t few = (rows + 15) / 16 * heads;
   const bool wide = head_dim == 128;
-  if ((rows <= 32 && !wide) || few <= (wide ? 64 : 128) || (few <= (wide ? 400 : 800) && seen <= 2200)) return 16;
+  if ((rows <= 32 && !wide) || few <= (wide ? 64 : 128) || (few <= (wide ? 400 : 800) && seen <= kWindowShort)) return 16;
   constexpr int32_t one = 16 * kAttnWaves;
   return wide || (rows + 2 * one - 1) / (2 * one) * heads < 256 ? one : 2 * one;
 }
@@ -1288,10 +1287,12 @@ int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim, int
 // workgroups a CU has (D = 64: 0.75, 0.9, 1.05, 1.2 us with one to four, which is what
 // the registers hold; eight waves, two; D = 128, three), and a join 3.5 us and what its
 // shares take to write and read.  Of 31 cases (32 to 1000 tokens, windows of 256 to
-// 4096, 16 to 376 workgroups, 1 to 16 splits) that is the best in 26 and 1.007 of it in
-// the mean; us here / as without a window: 512 tokens, D = 64, windows of 1000 and
-// 4096 26.8 / 26.9 and 52.2 / 64.1; 256, 4096 32.5 / 38.9; 1000, 1000 28.0 / 35.0;
-// D = 128, 512 tokens, 256 and 4096 16.4 / 22.2 and 66.4 / 79.7.
+// 4096, 16 to 376 workgroups, 1 to 16 splits) that is the best in 21 and 1.014 of it in
+// the mean (rounded up to whole blocks a split 26 and 1.007, but then a longer window
+// may take fewer splits, and the workspace is to grow with it).  us, here / as without
+// a window: 512 tokens, D = 64, windows of 512, 1000, 4096 19.0 / 20.6, 28.7 / 26.9,
+// 52.2 / 64.1; 256, 4096 32.5 / 38.9; 1000, 1000 28.0 / 35.0; D = 128, 512 tokens, 256
+// and 4096 16.4 / 22.2 and 64.6 / 79.7.
 int32_t kv4_attn_window_splits(int32_t tile_rows, int64_t workgroups, int64_t max_seen, int head_dim) {
   const bool few = tile_rows <= 16;
   if (workgroups >= (few ? 256 : 512)) return 1;
@@ -1300,12 +1301,13 @@ int32_t kv4_attn_window_splits(int32_t tile_rows, int64_t workgroups, int64_t ma
   const int64_t fit = eight ? 512 : head_dim == 64 ? 1024 : 768;
   const int64_t first = head_dim == 64 && !eight ? 600 : 400, more = eight ? 200 : head_dim == 64 ? 150 : 250;  // ns
   const int64_t blocks = max_seen / kKv4Block + 2;
-  int64_t best = 1, least = std::numeric_limits<int64_t>::max();
+  // times n, exact: a / n + join
+  int64_t best = 0, best_a = 0, best_join = 0;
   for (int64_t n = 1; n == 1 || (n * workgroups <= fit && 2 * n <= blocks); n += 1 + n / 16) {
     const int64_t total = n * workgroups;
-    const int64_t time = (blocks + n - 1) / n * (first + more * ((total + 255) / 256)) +
-                         (n == 1 ? 0 : 3500 + total * tile_rows * head_dim / 800);
-    if (time < least) best = n, least = time;
+    const int64_t a = blocks * (first + more * ((total + 255) / 256));
+    const int64_t join = n == 1 ? 0 : 3500 + total * tile_rows * head_dim / 800;
+    if (best == 0 || (a + join * n) * best < (best_a + best_join * best) * n) best = n, best_a = a, best_join = join;
   }
   return static_cast<int32_t>(best);
 }

@@ -358,6 +358,7 @@ struct AttnArgs {
 // shares that a sequence's cached tokens are split into; and the same with a window
 // (max_seen: what the rows of a workgroup see together).
 int32_t kv4_attn_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t max_q, int64_t max_kv);
+constexpr int64_t kWindowShort = 2200;  // tokens seen up to which more tiles count as few
 int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim, int64_t seen);
 int32_t kv4_attn_window_splits(int32_t tile_rows, int64_t workgroups, int64_t max_seen, int head_dim);
 int32_t kv4_attn_splits(int32_t tile_rows, int64_t workgroups, int64_t max_kv);
