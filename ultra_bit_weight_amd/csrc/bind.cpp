@@ -1,9 +1,9 @@
 // Argument checks and marshalling for Python of the entry points that a decode step
 // calls once a layer around its products.
 //
-// Their kernels take two to five microseconds, so the checks of the binding (shapes, types, devices, strides of
-// up to ten tensors) are done here on the tensors themselves: about 1 us a call
-// against 4 us through Python attributes.  No computation: every function checks,
+// Their kernels take two to five microseconds, so the checks of the binding (shapes,
+// types, devices, strides of up to ten tensors) are done here on the tensors
+// themselves: about 1 us a call against 4 us through Python attributes.  No computation: every function checks,
 // calls the C ABI (include/sherry.h) and returns its status.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

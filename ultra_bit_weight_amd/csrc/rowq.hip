@@ -12,7 +12,7 @@
 //
 // Bound by HBM: a row is read once and stays in its threads' registers through
 // both reductions.  T threads take a row, V runs of eight values each.  8192 rows of
-// 4096 in 16 bits with their residual 44.4 us, 5.3 TB/s, the rate of a large copy;
+// 4096 in 16 bits with their residual 44-46 us, 5.2 TB/s, the rate of a large copy;
 // 8192 rows of gate and up, 8192 each, 60 us, 5.6 TB/s; one row 2.75 and 3.15 us, a
 // launch and one load-reduce-store.
 #include <type_traits>

@@ -753,9 +753,10 @@ def kv4_append(cache, q, k, v, cos, sin, positions, slots, q_weight=None, k_weig
 
 def kv4_attn_workspace(cache, n_tokens, n_q_heads, n_seqs, max_q=None, max_kv=None, window=None, sinks=0):
     """A workspace for kv4_attn calls of these sizes (sherry_kv4_attn_workspace, with
-    a window sherry_kv4_attn_window_workspace); calls that may run at the same time need one each.  Without max_q it serves
-    calls without max_q, without max_kv any max_kv.  A smaller batch can need more
-    than a larger one: a program of changing batches asks for each, or holds
+    a window sherry_kv4_attn_window_workspace); calls that may run at the same time
+    need one each.  Without max_q it serves calls without max_q, without max_kv any
+    max_kv, with one every smaller one.  A smaller batch can need more than a larger
+    one: a program of changing batches asks for each, or holds
     KV4_ATTN_WORKSPACE_MAX bytes."""
     lib, kv = load(), _ANY_KV if max_kv is None else max_kv
     f, more = (lib.sherry_kv4_attn_workspace, ()) if window is None else (lib.sherry_kv4_attn_window_workspace, (window, sinks))
