@@ -398,23 +398,26 @@ __device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D 
   // of scores) of 2^24 on, and the largest weight be infinite or 0; the operation
   // costs 219 us against 213 for 2048 tokens over 8192, 113.1 against 112.0 for
   // ragged prompts, and where rows are few 1 % at most (12.2 against 12.0 for one
-  // token over 40000; 21.2 and 82.8 for 131072 and a batch as before).
-  auto score = [&](int i, float m, bool fold) {
-    float u = fold ? __builtin_fmaf(pr.kz(0, i), sumq[0], -m) : pr.kz(0, i) * sumq[0];
+  // token over 40000; 21.2 and 82.8 for 131072 and a batch as before).  Folded only
+  // where the maximum stays, nothing is infinite, but from scores of about 2^20 on
+  // equal keys weigh apart by where they lie (2048 tokens over 8192, D = 64, windows of
+  // 1000, 2048 and 4096 43.1, 65.2 and 117 us, 44.1, 67.4 and 122 as here).
+  auto score = [&](int i, float m) {
+    float u = pr.kz(0, i) * sumq[0];
 #pragma unroll
     for (int k = 1; k < NG; ++k) u = __builtin_fmaf(pr.kz(k, i), sumq[k], u);
 #pragma unroll
     for (int k = 0; k < NG; ++k) u = __builtin_fmaf(pr.ks(k, i), c[i >> 2][k][i & 3], u);
     if constexpr (!kReady) u *= pr.unit;
-    if (!fold) u -= m;
+    u -= m;
     if constexpr (kEdge) u = sees(t0 + 16 * (i >> 2) + (i & 3)) ? u : -__builtin_inff();
     return u;
   };
-  auto weights = [&](bool fold) {
+  auto weights = [&]() {
     top = 0.0f, sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(score(i, a.m, fold));
+      p[i] = __builtin_amdgcn_exp2f(score(i, a.m));
       sum += p[i];
     }
 #pragma unroll
@@ -425,12 +428,7 @@ __device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D 
         top = fmaxf(top, ps[k][i]);
       }
   };
-  // Many rows with a window fold it all the same, but not where the maximum is raised:
-  // a weight that rounding made too large brings the step there too, and the sum has
-  // the largest weight from there.  (2048 tokens, windows of 1000, 2048 and 4096: 39.9,
-  // 67.0, 122.7 -> 39.5, 65.0, 118.1; with D = 128 registers spill.)
-  constexpr bool kFold = kWin && kReady && D == 64;
-  weights(kFold);
+  weights();
   if (__builtin_expect(__any(top > kPTop || sum > kSumTop), 0)) {
     float mx = kNoMax;
 #pragma unroll
@@ -438,14 +436,14 @@ __device__ __forceinline__ void softmax_step(Acc<D>& a, const f32x4_t (&c)[2][D 
       float v = 5.9604644775390625e-8f;  // 2^-24
 #pragma unroll
       for (int k = 0; k < NG; ++k) v = fmaxf(v, pr.vs(k, i));
-      mx = fmaxf(mx, score(i, 0.0f, false) + __builtin_amdgcn_logf(v));  // log2
+      mx = fmaxf(mx, score(i, 0.0f) + __builtin_amdgcn_logf(v));  // log2
     }
     mx = fmaxf(mx, __shfl_xor(mx, 16));
     mx = fmaxf(mx, __shfl_xor(mx, 32));
     const float m_new = fmaxf(a.m, mx - kPExp);
     a.scale(__builtin_amdgcn_exp2f(a.m - m_new));
     a.m = m_new;
-    weights(false);
+    weights();
   }
   a.l += sum;
 #pragma unroll
@@ -901,11 +899,11 @@ __global__ __launch_bounds__(kAttnThreads, 2) void kv4_attn_rows_kernel(AttnArgs
 // 2048 tokens of 32 heads on 8 over 8192, D = 64, us, with one / two / four tiles
 // on four waves, and with eight waves: window 1000 48.1 / 47.7 / 63.0, 42.9; 4096
 // 158 / 155 / 144, 137; and with the softmax's wave priority 41.9 and 130, with page
-// numbers of 64 blocks at once 39.9 and 123, with the maximum folded 39.5 and 118 (590
-// Tflop/s); sixteen waves 40.1 and 119.  D = 128, five prompts of up to 1777 with a
-// window of 512: 87.2 / 94.2; eight waves 95.6, their registers spilled; with
-// page numbers of 64 blocks 85.3; with the priority 1 % more, but 2048 tokens over 8192,
-// windows of 512, 1000 and 4096, 37.6, 58.4, 196 -> 35.7, 55.7, 185.
+// numbers of 64 blocks at once 39.9 and 123 (570 Tflop/s); sixteen waves no faster.
+// D = 128, five prompts of up to 1777 with a window of 512: 87.2 / 94.2; eight waves
+// 95.6, their registers spilled; with page numbers of 64 blocks 85.3; with the priority
+// 1 % more, but 2048 tokens over 8192, windows of 512, 1000 and 4096, 37.6, 58.4, 196
+// -> 35.7, 55.7, 185.
 template <int D, int DT, int W>
 __global__ __launch_bounds__(W * kWave, W == 8 ? 4 : D == 128 ? 3 : 2) void kv4_attn_window_rows_kernel(AttnArgs a) {
   using L = Kv4Layout<D>;
