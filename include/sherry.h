@@ -129,7 +129,8 @@ sherry_status sherry_act_quant(const void* x, sherry_dtype x_dt, int64_t m, int6
  * in one pass, what stands before a layer's q|k|v and gate|up products:
  *   h[t, j]  = x[t, j] + residual[t, j]          (x without a residual)
  *   residual_out[t, j] = h[t, j], rounded to r_dt
- *   a[t]     = fp32(1 / sqrt(sum_j h[t, j]^2 / k + eps))   (this in fp64)
+ *   a[t]     = fp32(1 / sqrt(sum_j h[t, j]^2 / k + eps))   (this in fp64; the
+ *              largest fp32 for rows, with eps 0, whose factor would pass it)
  *   y[t, j]  = (h[t, j] a[t]) weight[j]
  *   scales, xq of y as in sherry_act_quant
  * Every step outside a[t] is one IEEE fp32 operation, so that codes, scales and
@@ -144,8 +145,8 @@ sherry_status sherry_act_quant(const void* x, sherry_dtype x_dt, int64_t m, int6
  *                  with 0)
  *   xq           : out, m x k int8, row stride ldq >= k; scales: out, m fp32
  * All aligned to their element sizes; rows of 16-byte aligned buffers with k a
- * multiple of 8 go fastest.  A row with a NaN or an infinity, or a sum past fp32,
- * has unspecified codes and scale; its neighbours keep theirs.
+ * multiple of 8 go fastest.  A row with a NaN or an infinity, or with an h or a y
+ * past fp32, has unspecified codes and scale; its neighbours keep theirs.
  * Errors: EINVAL null pointer, m < 0, k <= 0, eps; EDTYPE; ESHAPE k above 2^30, m
  * above 2^21 - 1 or a row stride below k; EALIGN. */
 sherry_status sherry_rms_norm_quant(const void* x, sherry_dtype x_dt, int64_t m, int64_t k, int64_t ldx,

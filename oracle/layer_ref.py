@@ -5,7 +5,8 @@ definitions in include/sherry.h; shares no code with the library.
 
 Readings: L1 h = x + r is one fp32 addition, the residual kept is h rounded to
 its type, and the norm is of h itself; L2 the sum of squares, mean, eps, root and
-reciprocal are fp64, rounded once to fp32; L3 (h a) w are two fp32 products; L4
+reciprocal are fp64, rounded once to fp32, to its largest number where they
+pass it; L3 (h a) w are two fp32 products; L4
 the codes are act_ref's (A1-A3); L5 the token at position p sees j <= p with
 j > p - window or j < sinks.
 """
@@ -20,7 +21,8 @@ def rms_norm(x, r, w, eps):
     if r is not None:
         h = h + np.asarray(r, np.float32)
     ss = np.array([sum_of_squares(row) for row in h])
-    a = (1.0 / np.sqrt(ss / h.shape[1] + np.float64(np.float32(eps)))).astype(np.float32)
+    a = 1.0 / np.sqrt(ss / h.shape[1] + np.float64(np.float32(eps)))
+    a = np.minimum(a, np.finfo(np.float32).max).astype(np.float32)
     return ((h * a[:, None]).astype(np.float32) * np.asarray(w, np.float32)).astype(np.float32), h
 
 

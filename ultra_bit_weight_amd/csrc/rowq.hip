@@ -173,13 +173,14 @@ __device__ __forceinline__ void put_codes(const float (&y)[V][8], float s, int8_
 
 // 1 / sqrt(mean + eps) within 2^-50: the hardware's estimate and two Newton steps (a
 // third of the latency of an exact root and quotient, which every row waits for).
-// Nothing at all under the root: the row is zeros, and so are its values.
+// Nothing at all under the root: the row is zeros, and so are its values.  Without eps a
+// row below 2^-128 has a factor past fp32: the largest one, so that zeros stay zeros.
 __device__ __forceinline__ float norm_factor(double ss, const NormQuantArgs& a) {
   const double x = __builtin_fma(ss, a.inv_k, static_cast<double>(a.eps));
   double y = __builtin_amdgcn_rsq(x);
 #pragma unroll
   for (int i = 0; i < 2; ++i) y = __builtin_fma(__builtin_fma(-x * y, y, 1.0), 0.5 * y, y);
-  return x > 0.0 ? static_cast<float>(y) : 0.0f;
+  return x > 0.0 ? fminf(static_cast<float>(y), 0x1.fffffep127f) : 0.0f;
 }
 
 template <int V>
