@@ -158,7 +158,10 @@ sherry_status sherry_rms_norm_quant(const void* x, sherry_dtype x_dt, int64_t m,
  * sherry_act_quant in one pass, what stands before its down product:
  *   y[t, j] = act(gate[t, j]) up[t, j]
  *   scales, xq of y as in sherry_act_quant
- * in fp32 (act within a few units in its last place).
+ * in fp32.  y is off by at most (10 + c max(0, -z)) 2^-24 of itself, 2^-119 of |up|
+ * and 2^-149, with z = gate, c = 2 (SiLU) or z = 2 sqrt(2 / pi) (g + 0.044715 g^3),
+ * c = 7 (GELU): the exponential of a far negative gate has its argument's rounding,
+ * and where it passes 2^126 (z below -87.3) nothing may be left of the value.
  *   gate, up   : m x k of x_dt (F32|F16|BF16), row strides ldg, ldu >= k (the two
  *                halves of a gate|up product: up = gate + k, both strides 2 k)
  *   activation : SHERRY_GATE_SILU, g / (1 + exp(-g)), or SHERRY_GATE_GELU_TANH,

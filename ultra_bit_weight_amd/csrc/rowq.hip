@@ -313,7 +313,10 @@ __global__ __launch_bounds__(row_block(T)) void rms_norm_quant_rows(NormQuantArg
 }
 
 // g / (1 + exp(-z)): SiLU with z = g, and GELU with z = 2 sqrt(2/pi) (g + 0.044715 g^3),
-// whose (1 + tanh(z/2)) / 2 this is without the cancellation.
+// whose (1 + tanh(z/2)) / 2 this is without the cancellation.  The exponential is the
+// hardware's, of one rounded product: its error grows with |z| where z < 0 (31 units in
+// the last place at -85, 84 of GELU at z = -87; 1.5 for z > 0).  Such a value is e^z times
+// an ordinary one, and codes keep seven bits of the row's largest.
 __device__ __forceinline__ float activate(float g, int act) {
   const float z = act == kGateSilu ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
