@@ -1277,10 +1277,25 @@ int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim, int
   return wide || (rows + 2 * one - 1) / (2 * one) * heads < 256 ? one : 2 * one;
 }
 
-// Windows are as long as one another, so there is nothing to even out where the
+// Short windows are as long as one another, so there is nothing to even out where the
 // workgroups fill the chip, and a join to save: few rows are not split from one
-// workgroup a CU on (48 tokens, window 2048, D = 128: 29.0 us, 33.6 in two; 128, window
-// 4096, D = 64: 58.3, 63.1), more from two.  Below that, the number of splits with the
+// workgroup a CU on, more from two.  Longer ones leave CUs idle, whose sequences are
+// shorter or which hold a workgroup less than others: few rows that see 4096 tokens are
+// split as without a window, with seven eighths of two workgroups a CU and more those
+// that see 8192.  us, whole / so, of uneven sequences of up to 12000 or (*) 32768:
+//   workgroups [256], D = 128: window 2048 20.7 / 21.9, 4096 30.9 / 30.7, 11000 64.8 / 57.0
+//     [320], D = 64: 2048 19.5 / 19.9, 4096 30.0 / 26.9, 8000 49.6 / 40.6, 20000* 121 / 73
+//     [320] of 16 rows, D = 64: 4096* 34.6 / 30.3, 20000* 137 / 83
+//     [384], D = 128: 2048 28.2 / 29.6, 4096 45.0 / 46.6, 6000 60.2 / 58.1, 11000 88 / 78
+//     [480], D = 128: 2048 29.3 / 35.3, 5000 55.0 / 59.7, 8000 86.2 / 85.6
+//     [512], D = 128: 8000* 108 / 112, 20000* 218 / 217, 32000* 269 / 254; D = 64: 11000
+//       56.9 / 52.9, 32000* 164 / 148
+//     [800], D = 64: 8000* 105 / 94, 32000* 247 / 234
+//     [1024], D = 64: 4096 52.5 / 57.2, 6000 76 / 81, 11000 115 / 110
+// and of equal ones [256], D = 128: 5000 33.8 / 36.1, 8000 51.8 / 53.2; [384], D = 64: 4096
+// 30.3 / 27.4, 8000 51 / 43; [512], D = 128: 8000* 117 / 124, 32000* 401 / 403; [800],
+// D = 64: 12000* 161 / 146.
+// More rows, below two workgroups a CU: the number of splits with the
 // least time by what was measured of many rows: a step of a block takes longer the more
 // workgroups a CU has (D = 64: 0.75, 0.9, 1.05, 1.2 us with one to four, which is what
 // the registers hold; eight waves, two; D = 128, three), and a join 3.5 us and what its
@@ -1293,8 +1308,11 @@ int32_t kv4_attn_window_tile_rows(int64_t rows, int64_t heads, int head_dim, int
 // and 4096 16.4 / 22.2 and 64.6 / 79.7.
 int32_t kv4_attn_window_splits(int32_t tile_rows, int64_t workgroups, int64_t max_seen, int head_dim) {
   const bool few = tile_rows <= 16;
-  if (workgroups >= (few ? 256 : 512)) return 1;
-  if (few) return kv4_attn_splits(tile_rows, workgroups, max_seen);
+  if (few) {
+    const bool whole = workgroups >= 256 && max_seen < (workgroups < 448 ? 4096 : 8192);
+    return whole ? 1 : kv4_attn_splits(tile_rows, workgroups, max_seen);
+  }
+  if (workgroups >= 512) return 1;
   const bool eight = tile_rows == 32 * kAttnWaves;
   const int64_t fit = eight ? 512 : head_dim == 64 ? 1024 : 768;
   const int64_t first = head_dim == 64 && !eight ? 600 : 400, more = eight ? 200 : head_dim == 64 ? 150 : 250;  // ns
