@@ -139,7 +139,8 @@ sherry_status sherry_act_quant(const void* x, sherry_dtype x_dt, int64_t m, int6
  *   x            : m x k of x_dt (F32|F16|BF16), row stride ldx >= k
  *   residual     : m x k of r_dt (F32|F16|BF16), row stride ldr, or NULL
  *   residual_out : m x k of r_dt, row stride ldro; NULL exactly if residual is.
- *                  It may be residual itself (with ldro = ldr)
+ *                  It may be residual itself (with ldro = ldr) or x itself (of
+ *                  r_dt, with ldro = ldx); outputs overlap no input otherwise
  *   weight       : k fp32
  *   eps          : finite, not negative (a row of zeros gives zeros, scale 1, also
  *                  with 0)

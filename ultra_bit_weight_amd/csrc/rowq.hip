@@ -201,7 +201,7 @@ constexpr int row_block(int t) { return t == kWave ? 4 * t : t; }
 // vector loads and stores at any address; a row's last run, where fewer than eight
 // values are left, is its last eight, of which those that the run before holds count
 // as zeros and are not stored (so that it does not matter whether the run before has
-// stored them, where r_out is r).  209 rows of 9213 values 5.2 us, 31 value by value;
+// stored them, where r_out is r or x).  209 rows of 9213 values 5.2 us, 31 value by value;
 // 8192 of 2049 34.6, 110; 8192 of gate and up, 8191 each, 66, 264 (8192 each, aligned,
 // 60).
 template <bool kLoose, int V>
@@ -427,8 +427,8 @@ __global__ __launch_bounds__(kLong) void rms_norm_quant_long(NormQuantArgs a, in
   }
   const float s = act_scale(RowTeam<kLong>::max(amax, wmax));
   if (threadIdx.x == 0) gmem(a.scales)[row] = s;
-  // (a thread reads the values of r that count for it where it writes r_out, which may
-  // be the same memory)
+  // (a thread reads the values of r and x that count for it where it writes r_out, which
+  // may be the same memory)
   for (int c0 = first; c0 < k; c0 += V * kStep) {
     values(c0, h);
     if constexpr (RB > 0) put_sum<RB, true, V>(a, row, c0, kStep, rdt, h);
