@@ -245,10 +245,13 @@ void launch_xy(AppendArgs& p, hipStream_t stream) {
   const int64_t kv = (n + 2 * kKv4Block - 2) / kKv4Block * p.g.n_kv_heads;
   const bool many = q_blocks(kAppendHeads) >= 1024;
   const int64_t total = kv + q_blocks(many ? kAppendHeads : 1);
-  // Where the chip holds the whole launch at once, k and v, whose way is longest, go
-  // first (2048 tokens, D = 64: 7.2 us, 7.4 evenly mixed); else they are spread over it
-  // (8192 tokens, D = 128: 31.2 us, 32.3 first; of fp32 43.9, 46.5): a 32-bit fraction,
-  // rounded up, so that each step is 0 or 1 and all are there by the end.
+  // k and v, whose way is longest, go first up to about two fills of the chip (at 71 to
+  // 96 registers it holds 1280 to 1792 workgroups); beyond, they are spread over the
+  // launch.  Time spread over time first, of 27 cases of 1100 to 8192 tokens: 1.01 to 1.16
+  // up to 1134 workgroups, 0.98 to 1.07 (mean 1.03) of 1500 to 2300, 0.99 to 1.04 around
+  // 2600, 0.97, 1.04, 0.97 at 2759, 3088, 3447, 0.94 to 0.98 from 4100 on (8192 tokens, D =
+  // 128: 30.8 us, 31.8 first; of fp32 44.2, 47.0).  A 32-bit fraction, rounded up, so that
+  // each step is 0 or 1 and all are there by the end.
   p.kv_blocks = static_cast<uint32_t>(kv);
   if (total > kAtOnce) p.kv_share = static_cast<uint32_t>(((static_cast<uint64_t>(kv) << 32) + total - 1) / total);
   p.stream = n * p.a.q.heads * D * act_bytes(YDT) > kStreamBytes;

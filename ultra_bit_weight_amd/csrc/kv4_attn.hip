@@ -215,7 +215,10 @@ __device__ __forceinline__ void load_p(const uint8_t* blk, int g, Params<D>& p) 
 // The blocks of cached tokens that a workgroup walks, numbered without a gap.
 // With a window these are the blocks that hold sinks, then those from the first
 // row's window on; without one, all of them up to the last row's position.
-// `whole` to `whole_end`: blocks of which every row sees all.
+// `whole` to `whole_end`: blocks of which every row sees all, from the last row's window
+// on.  (Blocks of sinks before it are tested score by score, those too of which every row
+// sees all: 2048 tokens over 8192, D = 64, 40.4 us with a window of 1000 and 20 sinks, 48.6
+// with 200, where a window of 1200 takes 44.2, and 81 with 1000, one of 2000 66.)
 template <bool kWin>
 struct Walk {
   int n;                 // blocks
