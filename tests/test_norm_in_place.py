@@ -22,6 +22,13 @@ def test_binding_refuses_x_of_another_shape():
         sherry.rms_norm_quant(x[:1], w, residual=r[:1], residual_out=wide.view(4, 80)[:1, :64])
 
 
+def test_no_rows_overlap_nothing():
+    """Tensors of no rows lie nowhere, all of them: types and strides may differ."""
+    w, x, r = torch.ones(64), torch.zeros(0, 64).half(), torch.zeros(0, 64)
+    with pytest.raises(ValueError, match="on the GPU"):
+        sherry.rms_norm_quant(x, w, residual=r, residual_out=torch.zeros(0, 64))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("m,k", [(3, 5), (300, 520), (2000, 513), (9, 2056), (90, 16385), (40, 40001)])
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -37,3 +44,11 @@ def test_sum_over_x(gpu_lib, m, k, dtype):
         assert got[2] is mine
         for a, b in zip(want, got):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_no_rows(gpu_lib):
+    say("no rows")
+    x, r = torch.zeros(0, 64, device=DEV).half(), torch.zeros(0, 64, device=DEV)
+    q, s, ro = gpu_lib.rms_norm_quant(x, torch.ones(64, device=DEV), residual=r)
+    assert q.shape == (0, 64) and s.shape == (0,) and ro.shape == (0, 64) and ro.dtype == torch.float32

@@ -273,7 +273,7 @@ PyObject* norm_quant(PyObject* const* a) {
     rm = matrix(a[2], "residual", {m, k}, r.scalar_type(), dev);
     om = matrix(a[4], "residual_out", {m, k}, r.scalar_type(), dev);
     if (om.p == rm.p && om.ld != rm.ld) value_error("residual_out begins where residual does, with another row stride");
-    if (om.p == xm.p && (om.ld != xm.ld || r.scalar_type() != x.scalar_type()))
+    if (m > 0 && om.p == xm.p && (om.ld != xm.ld || r.scalar_type() != x.scalar_type()))
       value_error("residual_out begins where x does, with another row stride or dtype");
   } else if (!none(a[4])) {
     value_error("residual_out needs residual");

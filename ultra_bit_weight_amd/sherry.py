@@ -638,8 +638,8 @@ def rms_norm_quant(x, weight, residual=None, eps=1e-6, residual_out=None, q_out=
 
     x [m, k] (fp32, fp16 or bf16, unit column stride), weight fp32 [k], residual
     [m, k] of a type of its own or None; residual_out (the sum in the residual's
-    type) may be residual or, of one type with it, x itself.  Returns (codes int8 [m, k], scales fp32 [m],
-    residual_out or None)."""
+    type) may be residual or, of one type with it, x itself.  Returns (codes int8
+    [m, k], scales fp32 [m], residual_out or None)."""
     q_out, scale_out = _quant_outs(x, q_out, scale_out)
     if residual is not None and residual_out is None:
         residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
